@@ -56,7 +56,8 @@ typedef enum {
     GPTQ_ERR_TIMEOUT = 7,  /* a kernel gave up a bounded wait (see gptq_device_error)  */
     GPTQ_ERR_ALIAS = 8,    /* the output overlaps an input                            */
     GPTQ_ERR_KERNEL = 9,   /* kernel_id names no kernel, or one that cannot take M     */
-    GPTQ_ERR_INDEX = 10    /* a g_idx entry outside 0 .. n_groups-1 (device-reported) */
+    GPTQ_ERR_INDEX = 10    /* a g_idx entry, experts' offset or row's place out of range
+                              (device-reported, see gptq_device_error)                */
 } gptq_status;
 
 /* Kernel identifiers reported by gptq_w4a16_select and accepted by
@@ -75,6 +76,8 @@ typedef enum {
 #define GPTQ_MAX_LORA_RANK 256 /* largest adapter rank of gptq_w4a16_gemm_lora */
 #define GPTQ_LORA_SCRATCH_BYTES (8 << 20) /* T buffer of gptq_w4a16_gemm_lora_noalloc */
 #define GPTQ_GIDX_MAX_GROUPS 640 /* scale rows of gptq_w4a16_gemm_gidx (a tile per CTA) */
+#define GPTQ_MOE_MAX_EXPERTS 1024 /* experts of a mixture-of-experts layer on one GPU */
+#define GPTQ_MOE_MAX_TOPK 64   /* experts chosen per token */
 
 /*
  * Y = X . dequant(qweight, scales).
@@ -250,6 +253,98 @@ GPTQ_API int gptq_w4a16_gemm_gidx(const uint16_t* x, const int32_t* qweight,
                                   const uint16_t* scales, const int32_t* g_idx, int64_t M,
                                   int64_t K, int64_t N, int64_t n_groups, uint16_t* y,
                                   void* stream);
+
+/*
+ * Mixture-of-experts layers whose experts are W4A16 linears.  A router (the
+ * caller's) chooses topk experts per token; the entries below gather the
+ * tokens into expert order, run every expert's linear on its rows in one
+ * call, and sum the rows back into tokens, with the gradients that a training
+ * step takes through them (the packed weights stay frozen, as with a LoRA
+ * adapter).  Nothing about the routing has to reach the host: the calls are
+ * stream-ordered and can be captured into a CUDA graph whose replays see new
+ * routings.
+ *
+ * gptq_moe_sort: the (token, choice) pairs p = m * topk + j sorted by expert,
+ * stably, and the tokens' rows in that order.
+ *   x          [M, H]       FP16 bits, H > 0, H % 8 == 0, H <= GPTQ_MAX_K
+ *   expert_ids [M, topk]    int32 (id_bytes 4) or int64 (id_bytes 8); an id
+ *                           outside 0 .. E-1 (as -1, or an expert of another
+ *                           GPU) drops its pair; a token may name an expert
+ *                           more than once
+ *   topk       1 .. GPTQ_MOE_MAX_TOPK, M * topk <= GPTQ_MAX_M
+ *   E          1 .. GPTQ_MOE_MAX_EXPERTS
+ *   x_sorted   [M * topk, H] FP16 bits, written: row dest[p] = x row m; the
+ *                           rows from offsets[E] on keep what they hold
+ *   offsets    [E + 1]      int32, written: expert e's rows are offsets[e] ..
+ *                           offsets[e + 1] - 1 (M == 0: all zero)
+ *   dest       [M, topk]    int32, written: the row of pair p, -1 if dropped
+ * The three outputs must not overlap each other or an input.
+ */
+GPTQ_API int gptq_moe_sort(const uint16_t* x, const void* expert_ids, int32_t id_bytes,
+                           int64_t M, int64_t H, int64_t topk, int64_t E, uint16_t* x_sorted,
+                           int32_t* offsets, int32_t* dest, void* stream);
+
+/*
+ * out[m] = fp16(sum_j weights[m, j] * y_sorted[dest[m, j]]), the sum in FP32
+ * in the order of j; dropped pairs (dest < 0) add nothing, a token without
+ * pairs becomes zero.
+ *   y_sorted [R, H] FP16 bits; dest [M, topk] int32 as gptq_moe_sort wrote it;
+ *   weights  [M, topk] FP32, or NULL for ones: with dx_sorted in place of
+ *            y_sorted that is the gradient of gptq_moe_sort's x
+ *   out      [M, H] FP16 bits, written; must not overlap an input
+ * An entry of dest of R or more is reported by gptq_device_error as
+ * GPTQ_ERR_INDEX and treated as dropped.  M == 0 enqueues nothing.
+ */
+GPTQ_API int gptq_moe_combine(const uint16_t* y_sorted, const int32_t* dest,
+                              const float* weights, int64_t M, int64_t H, int64_t topk,
+                              int64_t R, uint16_t* out, void* stream);
+
+/*
+ * The gradients of gptq_moe_combine with weights:
+ *   dy_sorted[dest[m, j]] = fp16(weights[m, j] * dout[m])      [R, H] FP16 bits
+ *   dweights[m, j] = <dout[m], y_sorted[dest[m, j]]>           [M, topk] FP32
+ * dweights is 0 for a dropped pair; rows of dy_sorted that no pair names keep
+ * what they hold.  The entries of dest that are not negative must differ from
+ * each other, as gptq_moe_sort's do.  dest entries of R or more as in
+ * gptq_moe_combine.  The outputs must not overlap each other or an input.
+ */
+GPTQ_API int gptq_moe_combine_backward(const uint16_t* dout, const uint16_t* y_sorted,
+                                       const int32_t* dest, const float* weights, int64_t M,
+                                       int64_t H, int64_t topk, int64_t R, uint16_t* dy_sorted,
+                                       float* dweights, void* stream);
+
+/*
+ * Every expert's linear on its own rows:
+ *   y_sorted[r] = x_sorted[r] . dequant(qweight[e], scales[e]),
+ *   offsets[e] <= r < offsets[e + 1]
+ *   x_sorted [R, K] FP16 bits; qweight [E, K/8, N] int32 and scales [E,
+ *   n_groups, N] FP16 bits, each expert's as gptq_w4a16_gemm takes them;
+ *   offsets  [E + 1] int32, device, ascending within 0 .. R (as gptq_moe_sort
+ *            wrote it); an expert may have no rows
+ *   y_sorted [R, N] FP16 bits, written in the rows of the experts; the other
+ *            rows keep what they hold; must not overlap an input
+ * Offsets out of order or range are clamped for reading (no access outside
+ * the tensors) and reported as GPTQ_ERR_INDEX by gptq_device_error; the
+ * output is then undefined.  Other limits, checks and errors as
+ * gptq_w4a16_gemm with M = R, plus GPTQ_ERR_SHAPE for E out of range and
+ * GPTQ_ERR_NULL for NULL offsets.  R == 0 enqueues nothing.
+ */
+GPTQ_API int gptq_w4a16_gemm_experts(const uint16_t* x_sorted, const int32_t* qweight,
+                                     const uint16_t* scales, const int32_t* offsets, int64_t R,
+                                     int64_t K, int64_t N, int64_t E, int32_t group,
+                                     uint16_t* y_sorted, void* stream);
+
+/*
+ * The gradient of gptq_w4a16_gemm_experts with respect to its rows:
+ *   dx_sorted[r] = dy_sorted[r] . dequant(qweight[e], scales[e])^T
+ * dy_sorted [R, N] FP16 bits; dx_sorted [R, K] FP16 bits, written in the rows
+ * of the experts.  FP32 accumulation, one rounding.  Limits, checks and
+ * errors as gptq_w4a16_gemm_experts.
+ */
+GPTQ_API int gptq_w4a16_gemm_experts_dx(const uint16_t* dy_sorted, const int32_t* qweight,
+                                        const uint16_t* scales, const int32_t* offsets,
+                                        int64_t R, int64_t K, int64_t N, int64_t E,
+                                        int32_t group, uint16_t* dx_sorted, void* stream);
 
 /*
  * W[K, N] = dequant(qweight, scales) as FP16 bits, each value rounded once from

@@ -24,6 +24,8 @@ MAX_GROUPED = 8
 MAX_LORA_RANK = 256
 LORA_SCRATCH_BYTES = 8 << 20
 GIDX_MAX_GROUPS = 640
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_TOPK = 64
 GROUP_SIZES = (-1, 16, 32, 64, 128, 256, 512, 1024)
 
 STATUS = {0: "GPTQ_OK", 1: "GPTQ_ERR_NULL", 2: "GPTQ_ERR_SHAPE", 3: "GPTQ_ERR_GROUP",
@@ -35,6 +37,8 @@ STATUS = {0: "GPTQ_OK", 1: "GPTQ_ERR_NULL", 2: "GPTQ_ERR_SHAPE", 3: "GPTQ_ERR_GR
 EXPORTS = ("gptq_w4a16_gemm", "gptq_w4a16_gemm_kernel", "gptq_w4a16_gemm_decode_splits",
            "gptq_w4a16_gemm_grouped", "gptq_w4a16_gemm_asym", "gptq_w4a16_gemm_gidx",
            "gptq_w4a16_gemm_lora", "gptq_w4a16_gemm_lora_noalloc",
+           "gptq_moe_sort", "gptq_moe_combine", "gptq_moe_combine_backward",
+           "gptq_w4a16_gemm_experts", "gptq_w4a16_gemm_experts_dx",
            "gptq_dequant",
            "gptq_w4a16_select", "gptq_status_string", "gptq_device_error", "gptq_version")
 
@@ -75,6 +79,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.gptq_w4a16_gemm_gidx.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _p]
             lib.gptq_w4a16_gemm_lora_noalloc.argtypes = [_p, _p, _p, _i64, _i64, _i64, _i32,
                                                          _p, _p, _i64, _p, _p]
+            lib.gptq_moe_sort.argtypes = [_p, _p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p]
+            lib.gptq_moe_combine.argtypes = [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p]
+            lib.gptq_moe_combine_backward.argtypes = [_p, _p, _p, _p, _i64, _i64, _i64, _i64,
+                                                      _p, _p, _p]
+            experts_args = [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32, _p, _p]
+            lib.gptq_w4a16_gemm_experts.argtypes = experts_args
+            lib.gptq_w4a16_gemm_experts_dx.argtypes = experts_args
             lib.gptq_dequant.argtypes = [_p, _p, _i64, _i64, _i32, _p, _p]
             lib.gptq_w4a16_select.argtypes = [_i64, _i64, _i64, _i32,
                                               ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
@@ -86,6 +97,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                          "gptq_w4a16_gemm_decode_splits", "gptq_w4a16_gemm_grouped",
                          "gptq_w4a16_gemm_asym", "gptq_w4a16_gemm_gidx", "gptq_w4a16_gemm_lora",
                          "gptq_w4a16_gemm_lora_noalloc",
+                         "gptq_moe_sort", "gptq_moe_combine", "gptq_moe_combine_backward",
+                         "gptq_w4a16_gemm_experts", "gptq_w4a16_gemm_experts_dx",
                          "gptq_dequant",
                          "gptq_w4a16_select", "gptq_device_error"):
                 getattr(lib, name).restype = ctypes.c_int
@@ -365,6 +378,181 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
                                                 group, _ptr(lora_a), _ptr(lora_b), rank,
                                                 _ptr(out), _stream_handle(stream, dev)))
     return out
+
+
+def _require_moe(t, name: str, dtype, device, shape=None):
+    """The checks of _require and _check_shape in one pass: the token movement
+    calls last a few microseconds on the device, so their checks are kept
+    short."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream))
+
+
+def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
+             out: torch.Tensor | None = None, stream=None):
+    """The tokens' rows in the order of their experts.
+
+    x [M, H] FP16; expert_ids [M, topk] int32 or int64, the experts chosen for
+    each token (ids outside 0 .. n_experts - 1 drop the choice).  Returns
+    (x_sorted [M * topk, H], offsets [n_experts + 1] int32, dest [M, topk]
+    int32): expert e's rows are offsets[e] .. offsets[e + 1] - 1, choice j of
+    token m is row dest[m, j] (-1 if dropped), in the order of (m, j) within an
+    expert.  The rows from offsets[n_experts] on keep what `out` holds."""
+    lib = load()
+    dev = x.device
+    _require_moe(x, "x", torch.float16, dev)
+    id_dtype = torch.int64 if expert_ids.dtype == torch.int64 else torch.int32
+    _require_moe(expert_ids, "expert_ids", id_dtype, dev)
+    if x.dim() != 2 or expert_ids.dim() != 2 or expert_ids.shape[0] != x.shape[0]:
+        raise ValueError("x and expert_ids must be 2-D with one row per token")
+    M, H = x.shape
+    topk = expert_ids.shape[1]
+    if out is None:
+        out = torch.empty((M * topk, H), dtype=torch.float16, device=dev)
+    else:
+        _require_moe(out, "out", torch.float16, dev, (M * topk, H))
+    offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=dev)
+    dest = torch.empty((M, topk), dtype=torch.int32, device=dev)
+    _call(lib.gptq_moe_sort, dev, stream, x.data_ptr(), expert_ids.data_ptr(),
+          8 if id_dtype == torch.int64 else 4, M, H, topk, n_experts, out.data_ptr(),
+          offsets.data_ptr(), dest.data_ptr())
+    return out, offsets, dest
+
+
+def moe_combine(y_sorted: torch.Tensor, dest: torch.Tensor, weights: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[m] = fp16(sum_j weights[m, j] * y_sorted[dest[m, j]]), FP32 sums in
+    the order of j, dropped choices (dest -1) left out.  y_sorted [R, H] FP16,
+    dest [M, topk] int32 from moe_sort, weights [M, topk] FP32 or None for
+    ones (then it is moe_sort's gradient, applied to that of x_sorted)."""
+    lib = load()
+    dev = y_sorted.device
+    _require_moe(y_sorted, "y_sorted", torch.float16, dev)
+    _require_moe(dest, "dest", torch.int32, dev)
+    if y_sorted.dim() != 2 or dest.dim() != 2:
+        raise ValueError("y_sorted and dest must be 2-D")
+    M, topk = dest.shape
+    R, H = y_sorted.shape
+    if weights is not None:
+        _require_moe(weights, "weights", torch.float32, dev, (M, topk))
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.float16, device=dev)
+    else:
+        _require_moe(out, "out", torch.float16, dev, (M, H))
+    _call(lib.gptq_moe_combine, dev, stream, y_sorted.data_ptr(), dest.data_ptr(),
+          None if weights is None else weights.data_ptr(), M, H, topk, R, out.data_ptr())
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y_sorted: torch.Tensor, dest: torch.Tensor,
+                         weights: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    """The gradients of moe_combine with weights: (dy_sorted [R, H] FP16,
+    dweights [M, topk] FP32) from dout [M, H] FP16.  Rows that no entry of dest
+    names keep what `out` (the buffer of dy_sorted) holds; dweights is 0 for
+    dropped choices."""
+    lib = load()
+    dev = dout.device
+    _require_moe(dout, "dout", torch.float16, dev)
+    _require_moe(y_sorted, "y_sorted", torch.float16, dev)
+    _require_moe(dest, "dest", torch.int32, dev)
+    if dout.dim() != 2 or y_sorted.dim() != 2 or dest.dim() != 2:
+        raise ValueError("dout, y_sorted and dest must be 2-D")
+    M, topk = dest.shape
+    R, H = y_sorted.shape
+    if dout.shape != (M, H):
+        raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(M, H)}")
+    _require_moe(weights, "weights", torch.float32, dev, (M, topk))
+    if out is None:
+        out = torch.empty((R, H), dtype=torch.float16, device=dev)
+    else:
+        _require_moe(out, "out", torch.float16, dev, (R, H))
+    dweights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+    _call(lib.gptq_moe_combine_backward, dev, stream, dout.data_ptr(), y_sorted.data_ptr(),
+          dest.data_ptr(), weights.data_ptr(), M, H, topk, R, out.data_ptr(),
+          dweights.data_ptr())
+    return out, dweights
+
+
+def experts_shapes(rows, qweight, scales, offsets, group: int,
+                   gradient: bool = False) -> tuple[int, int, int, int]:
+    """(R, K, N, E) of an experts' product, after checking qweight [E, K/8, N],
+    scales [E, n_groups(K, group), N], offsets [E + 1] and rows [R, K] (or
+    [R, N], for the gradient).  As in layer_shapes, an unsupported group is
+    left to the library."""
+    if rows.dim() != 2 or qweight.dim() != 3 or scales.dim() != 3 or offsets.dim() != 1:
+        raise ValueError("need 2-D rows, 3-D qweight and scales, 1-D offsets")
+    E, K, N = qweight.shape[0], 8 * qweight.shape[1], qweight.shape[2]
+    R, width = rows.shape
+    if width != (N if gradient else K):
+        raise ValueError(f"rows have {width} columns, expected {N if gradient else K}")
+    if offsets.shape[0] != E + 1:
+        raise ValueError(f"offsets has shape {tuple(offsets.shape)}, expected {(E + 1,)}")
+    if group in GROUP_SIZES and K > 0 and scales.shape != (E, n_groups(K, group), N):
+        raise ValueError(f"scales has shape {tuple(scales.shape)}, expected "
+                         f"{(E, n_groups(K, group), N)} for K={K}, group={group}")
+    return R, K, N, E
+
+
+def _experts(fn, rows, qweight, scales, offsets, group, out, stream, gradient, name):
+    dev = qweight.device
+    _require_moe(qweight, "qweight", torch.int32, dev)
+    _require_moe(scales, "scales", torch.float16, dev)
+    _require_moe(offsets, "offsets", torch.int32, dev)
+    _require_moe(rows, name, torch.float16, dev)
+    R, K, N, E = experts_shapes(rows, qweight, scales, offsets, group, gradient)
+    shape = (R, K if gradient else N)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float16, device=dev)
+    else:
+        _require_moe(out, "out", torch.float16, dev, shape)
+    _call(fn, dev, stream, rows.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
+          offsets.data_ptr(), R, K, N, E, group, out.data_ptr())
+    return out
+
+
+def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                 offsets: torch.Tensor, group: int, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Every expert's linear on its own rows: y_sorted[r] = x_sorted[r] .
+    dequant(qweight[e], scales[e]) for offsets[e] <= r < offsets[e + 1].
+    x_sorted [R, K] FP16 and offsets [E + 1] int32 as moe_sort returns them,
+    qweight [E, K/8, N] int32, scales [E, n_groups, N] FP16.  Rows that belong
+    to no expert keep what `out` holds."""
+    return _experts(load().gptq_w4a16_gemm_experts, x_sorted, qweight, scales, offsets, group,
+                    out, stream, False, "x_sorted")
+
+
+def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                    offsets: torch.Tensor, group: int, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """The gradient of gemm_experts with respect to x_sorted: dx_sorted[r] =
+    dy_sorted[r] . dequant(qweight[e], scales[e])^T, [R, K] FP16 from dy_sorted
+    [R, N] FP16 (the packed weights are frozen and have no gradient)."""
+    return _experts(load().gptq_w4a16_gemm_experts_dx, dy_sorted, qweight, scales, offsets,
+                    group, out, stream, True, "dy_sorted")
 
 
 def dequant(qweight: torch.Tensor, scales: torch.Tensor, group: int,

@@ -224,6 +224,51 @@ int lora_impl(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
   return GPTQ_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes of the token movement entries: M tokens of width H, topk choices.
+int check_moe(int64_t M, int64_t H, int64_t topk) {
+  if (M < 0 || H <= 0 || H % 8 != 0 || H > GPTQ_MAX_K || topk < 1 || topk > GPTQ_MOE_MAX_TOPK)
+    return GPTQ_ERR_SHAPE;
+  if (M > GPTQ_MAX_M || M * topk > GPTQ_MAX_M) return GPTQ_ERR_SHAPE;
+  return GPTQ_OK;
+}
+
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return GPTQ_OK;
+  cudaGetLastError();
+  return GPTQ_ERR_CUDA;
+}
+
+// The experts' products: in [R, K] -> out [R, N], or the gradient in [R, N]
+// -> out [R, K].
+int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* scales,
+                 const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
+                 int32_t group, uint16_t* out, void* stream, bool gradient) {
+  int st = check_shape(R, K, N, group);
+  if (st != GPTQ_OK) return st;
+  if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
+  if (!qweight || !scales || !offsets) return GPTQ_ERR_NULL;
+  if (R == 0) return GPTQ_OK;
+  if (!in || !out) return GPTQ_ERR_NULL;
+  if (!aligned16(in) || !aligned16(qweight) || !aligned16(scales) || !aligned16(out) ||
+      !aligned4(offsets))
+    return GPTQ_ERR_ALIGN;
+  const int64_t ib = R * (gradient ? N : K) * 2, ob = R * (gradient ? K : N) * 2;
+  if (overlaps(out, ob, in, ib) || overlaps(out, ob, qweight, E * (K / 8) * N * 4) ||
+      overlaps(out, ob, scales, E * num_groups(K, group) * N * 2) ||
+      overlaps(out, ob, offsets, (E + 1) * 4))
+    return GPTQ_ERR_ALIAS;
+  const DeviceInfo* dev = nullptr;
+  st = query_device(&dev);
+  if (st != GPTQ_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int gs = group_shift_of(group);
+  return status_of(
+      gradient ? launch_experts_dx(in, qweight, scales, offsets, out, R, K, N, E, gs, s, *dev)
+               : launch_experts_pair(in, qweight, scales, offsets, out, R, K, N, E, gs, s, *dev));
+}
+
 }  // namespace
 }  // namespace gptq
 
@@ -376,6 +421,100 @@ int gptq_w4a16_gemm_lora_noalloc(const uint16_t* x, const int32_t* qweight,
                    stream);
 }
 
+int gptq_moe_sort(const uint16_t* x, const void* expert_ids, int32_t id_bytes, int64_t M,
+                  int64_t H, int64_t topk, int64_t E, uint16_t* x_sorted, int32_t* offsets,
+                  int32_t* dest, void* stream) {
+  int st = check_moe(M, H, topk);
+  if (st != GPTQ_OK) return st;
+  if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
+  if (id_bytes != 4 && id_bytes != 8) return GPTQ_ERR_SHAPE;
+  if (!offsets) return GPTQ_ERR_NULL;
+  if (M > 0 && (!x || !expert_ids || !x_sorted || !dest)) return GPTQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(x_sorted) || !aligned4(offsets) || !aligned4(dest) ||
+      (reinterpret_cast<uintptr_t>(expert_ids) & (uintptr_t)(id_bytes - 1)) != 0)
+    return GPTQ_ERR_ALIGN;
+  const int64_t P = M * topk;
+  const void* outs[3] = {x_sorted, offsets, dest};
+  const int64_t out_bytes[3] = {P * H * 2, (E + 1) * 4, P * 4};
+  for (int i = 0; i < 3; ++i) {
+    if (overlaps(outs[i], out_bytes[i], x, M * H * 2) ||
+        overlaps(outs[i], out_bytes[i], expert_ids, P * id_bytes))
+      return GPTQ_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], out_bytes[i], outs[j], out_bytes[j])) return GPTQ_ERR_ALIAS;
+  }
+  const DeviceInfo* dev = nullptr;
+  st = query_device(&dev);
+  if (st != GPTQ_OK) return st;
+  return status_of(launch_moe_sort(x, expert_ids, id_bytes, M, H, (int)topk, (int)E, x_sorted,
+                                   offsets, dest, static_cast<cudaStream_t>(stream), *dev));
+}
+
+int gptq_moe_combine(const uint16_t* y_sorted, const int32_t* dest, const float* weights,
+                     int64_t M, int64_t H, int64_t topk, int64_t R, uint16_t* out,
+                     void* stream) {
+  int st = check_moe(M, H, topk);
+  if (st != GPTQ_OK) return st;
+  if (R < 0 || R > GPTQ_MAX_M) return GPTQ_ERR_SHAPE;
+  if (M == 0) return GPTQ_OK;
+  if (!dest || !out || (R > 0 && !y_sorted)) return GPTQ_ERR_NULL;
+  if (!aligned16(y_sorted) || !aligned16(out) || !aligned4(dest) || !aligned4(weights))
+    return GPTQ_ERR_ALIGN;
+  const int64_t ob = M * H * 2, pb = M * topk * 4;
+  if (overlaps(out, ob, y_sorted, R * H * 2) || overlaps(out, ob, dest, pb) ||
+      (weights && overlaps(out, ob, weights, pb)))
+    return GPTQ_ERR_ALIAS;
+  const DeviceInfo* dev = nullptr;
+  st = query_device(&dev);
+  if (st != GPTQ_OK) return st;
+  return status_of(launch_moe_combine(y_sorted, dest, weights, M, H, (int)topk, R, out,
+                                      static_cast<cudaStream_t>(stream), *dev));
+}
+
+int gptq_moe_combine_backward(const uint16_t* dout, const uint16_t* y_sorted,
+                              const int32_t* dest, const float* weights, int64_t M, int64_t H,
+                              int64_t topk, int64_t R, uint16_t* dy_sorted, float* dweights,
+                              void* stream) {
+  int st = check_moe(M, H, topk);
+  if (st != GPTQ_OK) return st;
+  if (R < 0 || R > GPTQ_MAX_M) return GPTQ_ERR_SHAPE;
+  if (M == 0) return GPTQ_OK;
+  if (!dout || !dest || !weights || !dweights || (R > 0 && (!y_sorted || !dy_sorted)))
+    return GPTQ_ERR_NULL;
+  if (!aligned16(dout) || !aligned16(y_sorted) || !aligned16(dy_sorted) || !aligned4(dest) ||
+      !aligned4(weights) || !aligned4(dweights))
+    return GPTQ_ERR_ALIGN;
+  const int64_t gb = M * H * 2, rb = R * H * 2, pb = M * topk * 4;
+  const void* outs[2] = {dy_sorted, dweights};
+  const int64_t out_bytes[2] = {rb, pb};
+  for (int i = 0; i < 2; ++i)
+    if (overlaps(outs[i], out_bytes[i], dout, gb) || overlaps(outs[i], out_bytes[i], y_sorted, rb) ||
+        overlaps(outs[i], out_bytes[i], dest, pb) || overlaps(outs[i], out_bytes[i], weights, pb))
+      return GPTQ_ERR_ALIAS;
+  if (overlaps(dy_sorted, rb, dweights, pb)) return GPTQ_ERR_ALIAS;
+  const DeviceInfo* dev = nullptr;
+  st = query_device(&dev);
+  if (st != GPTQ_OK) return st;
+  return status_of(launch_moe_combine_backward(dout, y_sorted, dest, weights, M, H, (int)topk, R,
+                                               dy_sorted, dweights,
+                                               static_cast<cudaStream_t>(stream), *dev));
+}
+
+int gptq_w4a16_gemm_experts(const uint16_t* x_sorted, const int32_t* qweight,
+                            const uint16_t* scales, const int32_t* offsets, int64_t R, int64_t K,
+                            int64_t N, int64_t E, int32_t group, uint16_t* y_sorted,
+                            void* stream) {
+  return experts_impl(x_sorted, qweight, scales, offsets, R, K, N, E, group, y_sorted, stream,
+                      false);
+}
+
+int gptq_w4a16_gemm_experts_dx(const uint16_t* dy_sorted, const int32_t* qweight,
+                               const uint16_t* scales, const int32_t* offsets, int64_t R,
+                               int64_t K, int64_t N, int64_t E, int32_t group,
+                               uint16_t* dx_sorted, void* stream) {
+  return experts_impl(dy_sorted, qweight, scales, offsets, R, K, N, E, group, dx_sorted, stream,
+                      true);
+}
 
 int gptq_dequant(const int32_t* qweight, const uint16_t* scales, int64_t K, int64_t N,
                  int32_t group, uint16_t* w_out, void* stream) {
@@ -425,7 +564,7 @@ const char* gptq_status_string(int status) {
     case GPTQ_ERR_TIMEOUT: return "a kernel gave up a bounded wait";
     case GPTQ_ERR_ALIAS: return "output overlaps an input";
     case GPTQ_ERR_KERNEL: return "kernel id or split count not valid for this call";
-    case GPTQ_ERR_INDEX: return "a g_idx entry outside 0 .. n_groups - 1";
+    case GPTQ_ERR_INDEX: return "an index out of range (g_idx, experts' offsets, or a row's place)";
     default: return "unknown status";
   }
 }

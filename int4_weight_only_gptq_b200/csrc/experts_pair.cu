@@ -1,0 +1,636 @@
+// The experts' products on CTA pairs: for every expert e and its rows
+//   Y[rows of e] = X[rows of e] . dequant(qweight[e], scales[e])
+// and the gradient with respect to the rows,
+//   dX[rows of e] = dY[rows of e] . dequant(qweight[e], scales[e])^T,
+// with tcgen05.mma.cta_group::2.
+//
+// The transposed product of the pair prefill kernel (256 output columns per
+// CTA pair as the MMA's M, dequantised into TMEM; tokens as its N, half of the
+// token tile loaded by each CTA; persistent clusters walking the tiles), with
+// the token tiles cut from the experts' rows:
+//
+// * The experts' row counts are known on the device only.  Every CTA builds
+//   the same table of token tiles from the offsets (experts.cuh) and cluster c
+//   takes tiles c, c + clusters, ..., column pair fastest.
+// * A tile holds up to 256 rows of one expert; the MMA's width is the rows
+//   rounded up to 32, so an expert with few rows pays for those only.  The
+//   copy boxes of X come in 32, 64 and 128 rows per CTA for the same reason.
+//   Rows that a box reads past the tile belong to other experts (or read as
+//   zero past the tensor): each is a column of the accumulator of its own,
+//   which is never stored.
+// * Stores: 64-row blocks wholly inside the tile go through TMA, the others
+//   as 16-byte rows, so that no other expert's row is written.
+//
+// In the gradient the roles of K and N are exchanged: the pair's 256 columns
+// are k, the contraction runs over n.  The weight tile of a stage is the same
+// box of 16 packed rows x 128 columns, but a TMEM lane is now one k: its
+// thread reads every word of its packed row, picks its own nibble of two
+// neighbouring words with one byte permute, and multiplies them by the two
+// columns' scales.
+//
+// Every wait is bounded in time; on expiry the CTA records GPTQ_ERR_TIMEOUT
+// in the device error word and winds down.  Both CTAs always reach the final
+// cluster barrier, so neither leaves while the other may still signal it.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "experts.cuh"
+#include "gptq_w4a16.h"
+#include "kernels.h"
+#include "tc05.cuh"
+#include "tmap.h"
+
+namespace gptq {
+
+namespace {
+
+constexpr int BW = 128;   // output columns per CTA (TMEM lanes); 256 per pair (MMA M)
+constexpr int BK = 128;   // contraction per pipeline stage (eight k16 MMAs)
+constexpr int BT = 256;   // tokens per pair tile, at most
+constexpr int HT = BT / 2;  // ... loaded by each CTA
+constexpr int XS = 3;     // X ring stages (half tile per CTA)
+constexpr int WS = 4;     // weight-tile ring stages (qweight + scales)
+constexpr int AS = 4;     // A slots in TMEM (BK each)
+constexpr int DQ_GROUPS = 4;             // dequantisation groups: group g takes stages g mod 4
+constexpr int DQ_WARPS = 4 * DQ_GROUPS;  // one warp per TMEM lane quarter in each group
+constexpr int DQ_WARP0 = 3;  // warps 0, 1, 2: X producer, MMA issuer, weight producer
+constexpr int THREADS = (DQ_WARP0 + DQ_WARPS) * 32;
+constexpr int QW_STAGE_BYTES = BW * (BK / 8) * 4;  // 16 packed rows x 128 columns: 8 KB
+constexpr int QW_ROW_BYTES = BW * 4;
+constexpr int S_ROW_BYTES = BW * 2;                // one scale row of the tile: 256 B
+constexpr int S_STAGE_MAX_ROWS = BK / 16;          // group 16: eight rows per stage
+constexpr int W_STAGE_BYTES = QW_STAGE_BYTES + S_STAGE_MAX_ROWS * S_ROW_BYTES;
+constexpr int X_STAGE_BYTES = 2 * HT * 128;        // two 64-k halves of 128-byte rows
+constexpr int TPG = BT / DQ_GROUPS;                // tokens read out per group
+constexpr int Y_WARP_BYTES = TPG * 32 * 2;         // a warp's staging block: 64 tokens x 32 columns
+constexpr int W_OFF = XS * X_STAGE_BYTES;
+constexpr int Y_OFF = W_OFF + WS * W_STAGE_BYTES;
+constexpr int BAR_OFF = Y_OFF + DQ_WARPS * Y_WARP_BYTES;
+constexpr int TABLE_OFF = BAR_OFF + 512;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t D_COL = 0;              // accumulator: columns [0, BT)
+constexpr uint32_t A_COL = 256;            // A slots: [256, 256 + 4 * 64)
+constexpr uint32_t A_STAGE_COLS = BK / 2;  // two FP16 per 32-bit column
+constexpr uint16_t kPairMask = 0x3;        // both CTAs of the cluster
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr uint64_t kDrainLimitNs = 200000000ull;
+static_assert(A_COL + AS * A_STAGE_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(AS == DQ_GROUPS && WS % DQ_GROUPS == 0,
+              "stage g uses A slot g mod 4 and weight slot g mod WS, both of group g mod 4");
+
+using Table = ExpertTable<BT, 32>;
+static_assert(1024 + TABLE_OFF + Table::bytes(GPTQ_MOE_MAX_EXPERTS) <= 227 * 1024,
+              "shared memory per CTA");
+
+// Both CTAs hold the full set; xfull, afull and dempty are only used in the
+// even CTA.
+struct PairBarriers {
+  uint64_t xfull[XS];   // both halves of the X stage landed (even CTA)
+  uint64_t xempty[XS];  // pair MMAs reading the X stage done
+  uint64_t wfull[WS];   // this CTA's qweight and scale tiles landed
+  uint64_t wempty[WS];  // weight tiles read by this CTA's group warps
+  uint64_t afull[AS];   // A slot written by the group warps of both CTAs (even CTA)
+  uint64_t aempty[AS];  // pair MMAs reading the A slot done
+  uint64_t dfull;       // all MMAs of the current tile done
+  uint64_t dempty;      // accumulator read out by every group warp of both CTAs (even CTA)
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(PairBarriers) <= 512, "barrier area");
+
+// The boxes in which X is read: 32, 64 or 128 rows per CTA.
+struct XMaps {
+  CUtensorMap rows[3];
+};
+
+__device__ __forceinline__ int box_index(int n) { return n <= 64 ? 0 : (n <= 128 ? 1 : 2); }
+
+// The tiles of one cluster: tile = cluster + i * clusters for i = 0, 1, ...;
+// column pair fastest.
+struct Walk {
+  int cluster, clusters, n_pairs, tiles;
+  Table table;
+  __device__ int count() const {
+    return cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
+  }
+  // This CTA's first output column in tile i, and the token tile.
+  __device__ ExpertTile at(int i, uint32_t rank, int& o0) const {
+    const int tile = cluster + i * clusters;
+    o0 = (2 * (tile % n_pairs) + (int)rank) * BW;
+    return table.find(tile / n_pairs);
+  }
+};
+
+// C: the contraction length (K, or N in the gradient); O: the output width
+// (N, or K in the gradient).  scale_rows: scale rows that 128 k touch.
+// x3d: X is read through a [C/64][R][64] view, one copy per stage (C a
+// multiple of 64); otherwise through [R][C], one copy per 64-column half.
+template <bool DX>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    experts_pair_kernel(const __grid_constant__ XMaps x_maps,
+                        const __grid_constant__ CUtensorMap qw_map,
+                        const __grid_constant__ CUtensorMap s_map,
+                        const __grid_constant__ CUtensorMap y_map, const int32_t* offsets, int R,
+                        int C, int O, int E, int group_shift, int scale_rows, int x3d,
+                        int n_pairs, uint16_t* y, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  // 1024-byte aligned base; the same offset in both CTAs, so that one MMA
+  // descriptor and one barrier offset name the matching buffers of the pair
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* xs = smem;
+  PairBarriers* bar = reinterpret_cast<PairBarriers*>(smem + BAR_OFF);
+  volatile int* abort_flag = &bar->abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: even CTA (issues the MMAs), 1: odd CTA
+  const bool even = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < XS; ++s) {
+      mbar_init(&bar->xfull[s], 1);   // the even CTA's expect_tx; bytes from both CTAs
+      mbar_init(&bar->xempty[s], 1);  // one pair commit
+    }
+    for (int j = 0; j < WS; ++j) {
+      mbar_init(&bar->wfull[j], 1);
+      mbar_init(&bar->wempty[j], 4);      // the four warps of the slot's group
+    }
+    for (int j = 0; j < AS; ++j) {
+      mbar_init(&bar->afull[j], 2 * 4);   // the slot's group warps in both CTAs
+      mbar_init(&bar->aempty[j], 1);      // one pair commit
+    }
+    mbar_init(&bar->dfull, 1);                 // one pair commit per tile
+    mbar_init(&bar->dempty, 2 * DQ_WARPS);     // every group warp of both CTAs
+    bar->abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < 3; ++i) prefetch_tensormap(&x_maps.rows[i]);
+    prefetch_tensormap(&qw_map);
+    prefetch_tensormap(&s_map);
+    prefetch_tensormap(&y_map);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc_pair(&bar->tmem_base, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  // the offsets and X may come from the previous kernel of the stream
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Walk walk;
+  walk.cluster = (int)(blockIdx.x >> 1);
+  walk.clusters = (int)(gridDim.x >> 1);
+  walk.n_pairs = n_pairs;
+  walk.table.place(smem + TABLE_OFF, E);
+  walk.table.build(offsets, R, THREADS, err);
+  walk.tiles = walk.table.tiles() * n_pairs;
+  const int NT = walk.count();          // tiles of this cluster
+  const int KB = (C + BK - 1) / BK;     // stages per tile
+  const int G = NT * KB;                // stages of this cluster, over all its tiles
+  // both CTAs' barriers are initialised and TMEM is allocated before any
+  // thread signals the other CTA
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  // the even CTA's barriers that both CTAs signal
+  const uint32_t xfull_even = map_to_rank(smem_u32(&bar->xfull[0]), 0);
+  const uint32_t afull_even = map_to_rank(smem_u32(&bar->afull[0]), 0);
+  const uint32_t dempty_even = map_to_rank(smem_u32(&bar->dempty), 0);
+
+  if (warp == 0 || warp == 2) {
+    // ---------------- TMA producers: X half (warp 0), weights (warp 2) ----------------
+    if (lane == 0 && NT > 0) {
+      int it = 0, kb = 0, o0;
+      ExpertTile tt = walk.at(0, rank, o0);
+      int s = 0;
+      uint32_t ph = 0;
+      int issued = 0;
+      if (warp == 0) {
+        // The odd CTA's half of the token tile may lie wholly past the last
+        // row of X: then it loads nothing and the even CTA expects only its
+        // own bytes; the MMA reads stale shared memory for token columns that
+        // are never stored.
+        int box = box_index(tt.n);
+        bool odd_rows = tt.row0 + tt.n / 2 < R;
+        int row = tt.row0 + (int)rank * (tt.n / 2);
+        for (int g = 0; g < G; ++g) {
+          if (!mbar_wait_bounded(&bar->xempty[s], ph ^ 1u, abort_flag, kWaitLimitNs)) {
+            record_timeout(err, bar);
+            break;
+          }
+          uint8_t* dst = xs + s * X_STAGE_BYTES;
+          const uint32_t bar_c = xfull_even + 8u * (uint32_t)s;
+          const uint32_t half_bytes = 4096u << box;
+          const int c0 = kb * BK;
+          // the second 64-column half holds columns below C (else it is
+          // neither loaded nor multiplied)
+          const bool hi = c0 + 64 < C;
+          if (even)
+            mbar_arrive_expect_tx(&bar->xfull[s],
+                                  (odd_rows ? 2u : 1u) * ((x3d || hi) ? 2 * half_bytes
+                                                                      : half_bytes));
+          if (even || odd_rows) {
+            if (x3d) {
+              tma_load_3d_pair(dst, &x_maps.rows[box], 0, row, c0 / 64, bar_c);
+            } else {
+              tma_load_2d_pair(dst, &x_maps.rows[box], c0, row, bar_c);
+              if (hi)
+                tma_load_2d_pair(dst + half_bytes, &x_maps.rows[box], c0 + 64, row, bar_c);
+            }
+          }
+          ++issued;
+          if (++s == XS) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (++kb == KB) {
+            kb = 0;
+            if (++it < NT) {
+              tt = walk.at(it, rank, o0);
+              box = box_index(tt.n);
+              odd_rows = tt.row0 + tt.n / 2 < R;
+              row = tt.row0 + (int)rank * (tt.n / 2);
+            }
+          }
+        }
+        if (*abort_flag && even) {
+          // drain: wait for the last loads issued into each slot (the odd
+          // CTA's X loads complete on the even CTA's barriers, which the
+          // even CTA drains)
+          int never = 0;
+          for (int j = issued - 1; j >= 0 && j >= issued - XS; --j)
+            mbar_wait_bounded(&bar->xfull[j % XS], (uint32_t)(j / XS) & 1u, &never,
+                              kDrainLimitNs);
+        }
+      } else {
+        const uint32_t wbytes = QW_STAGE_BYTES + scale_rows * S_ROW_BYTES;
+        for (int g = 0; g < G; ++g) {
+          if (!mbar_wait_bounded(&bar->wempty[s], ph ^ 1u, abort_flag, kWaitLimitNs)) {
+            record_timeout(err, bar);
+            break;
+          }
+          uint8_t* wst = smem + W_OFF + s * W_STAGE_BYTES;
+          if (o0 < O) {
+            // first column and first k of the stage's weight tile
+            const int n0 = DX ? kb * BK : o0, k0 = DX ? o0 : kb * BK;
+            mbar_arrive_expect_tx(&bar->wfull[s], wbytes);
+            tma_load_3d(wst, &qw_map, n0, k0 / 8, tt.e, &bar->wfull[s]);
+            tma_load_3d(wst + QW_STAGE_BYTES, &s_map, n0, (int)((int64_t)k0 >> group_shift),
+                        tt.e, &bar->wfull[s]);
+          } else {
+            mbar_arrive(&bar->wfull[s]);  // padding CTA: no columns, nothing to load
+          }
+          ++issued;
+          if (++s == WS) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (++kb == KB) {
+            kb = 0;
+            if (++it < NT) tt = walk.at(it, rank, o0);
+          }
+        }
+        if (*abort_flag) {
+          int never = 0;
+          for (int j = issued - 1; j >= 0 && j >= issued - WS; --j)
+            mbar_wait_bounded(&bar->wfull[j % WS], (uint32_t)(j / WS) & 1u, &never,
+                              kDrainLimitNs);
+        }
+      }
+    }
+    __syncwarp();  // the whole warp reaches the cluster barrier below together
+  } else if (warp == 1) {
+    // ---------------- pair MMA issuer (even CTA) ----------------
+    if (even) {
+      bool ok = true;
+      int g = 0, it = 0;
+      for (; it < NT && ok; ++it) {
+        int o0;
+        const int n = walk.at(it, rank, o0).n;
+        const uint32_t idesc = idesc_f16_f32(2 * BW, n);
+        const uint32_t half_bytes = 4096u << box_index(n);
+        if (it > 0) {
+          // the previous tile's accumulator has been read out by every group
+          // warp of both CTAs
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->dempty, (uint32_t)(it - 1) & 1u,
+                                                         abort_flag, kWaitLimitNs));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        for (int kb = 0; kb < KB; ++kb, ++g) {
+          const int s = g % XS, a = g % AS;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar->xfull[s], (uint32_t)(g / XS) & 1u, abort_flag,
+                                            kWaitLimitNs) &&
+                              mbar_wait_bounded(&bar->afull[a], (uint32_t)(g / AS) & 1u,
+                                                abort_flag, kWaitLimitNs));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t b_desc0 = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES));
+          const uint32_t a_base = tmem + A_COL + a * A_STAGE_COLS;
+          const int nk = min(BK, C - kb * BK + 15) / 16;  // k16 steps holding columns below C
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              if (kk < nk)
+                mma_f16_ts_pair(tmem + D_COL, a_base + kk * 8,
+                                b_desc0 + (uint64_t)(((kk >> 2) * half_bytes +
+                                                      (kk & 3) * 32) >> 4),
+                                idesc, (kb | kk) != 0 ? 1u : 0u);
+            mma_commit_pair(&bar->xempty[s], kPairMask);
+            mma_commit_pair(&bar->aempty[a], kPairMask);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) mma_commit_pair(&bar->dfull, kPairMask);  // tile done
+        __syncwarp();
+      }
+      if (!ok) {
+        if (lane == 0) record_timeout(err, bar);
+        // wait for the MMAs already issued before anyone frees TMEM
+        if (elect_one()) mma_commit_pair(&bar->dfull, kPairMask);
+        __syncwarp();
+        int never = 0;
+        mbar_wait_bounded(&bar->dfull, (uint32_t)it & 1u, &never, kDrainLimitNs);
+      }
+    }
+    __syncwarp();  // the whole warp reaches the cluster barrier below together
+  } else {
+    // ---------------- dequantisation and accumulator read-out ----------------
+    const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
+    const int grp = (warp - DQ_WARP0) >> 2;  // stages g = grp mod DQ_GROUPS
+    const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
+    const int col = 32 * quarter + lane;     // this thread's TMEM lane: its output column
+    const int j = grp;                       // this group's A slot
+    uint8_t* ystage = smem + Y_OFF + (grp * 4 + quarter) * Y_WARP_BYTES;
+
+    // Reads out tile d's accumulator (this warp's 32 lanes x its group's TPG
+    // tokens), hands it back to the MMA warp, and stores the FP16 values
+    // through this warp's staging block.  False if the wait expired.
+    auto drain = [&](int d) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded<true>(&bar->dfull, (uint32_t)d & 1u,
+                                                           abort_flag, kWaitLimitNs)))
+        return false;
+      int o0;
+      const ExpertTile tt = walk.at(d, rank, o0);
+      const int live = min(TPG, tt.rows - grp * TPG);  // this group's tokens inside the tile
+      tc_fence_after();
+      uint32_t v0[32], v1[32];
+      if (live > 0) {
+        tmem_ld_32x32b_x32(tmem + lane_addr + D_COL + grp * TPG, v0);
+        tmem_ld_32x32b_x32(tmem + lane_addr + D_COL + grp * TPG + 32, v1);
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(dempty_even);  // the MMAs may overwrite it now
+      const int c0 = o0 + 32 * quarter;
+      if (live <= 0 || c0 >= O) return true;
+      if (lane == 0) bulk_wait_read_all();  // the block's previous store has read it
+      __syncwarp();
+      uint16_t* ys = reinterpret_cast<uint16_t*>(ystage);
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        ys[q * 32 + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(v0[q])));
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        ys[(32 + q) * 32 + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(v1[q])));
+      const int row = tt.row0 + grp * TPG;
+      if (live == TPG) {
+        fence_proxy_async_smem();  // the staging writes are visible to the store
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&y_map, ystage, c0, row);
+          bulk_commit_group();
+        }
+      } else {
+        // the tile ends inside the block: its rows only, 16 bytes at a time
+        __syncwarp();
+        for (int i = lane; i < 4 * live; i += 32) {
+          const int c = c0 + 8 * (i & 3);
+          if (c < O)
+            *reinterpret_cast<uint4*>(y + (int64_t)(row + (i >> 2)) * O + c) =
+                *reinterpret_cast<const uint4*>(ystage + 16 * i);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+
+    // forward: this thread's column in weight slot 0; gradient: its packed
+    // row, the byte and nibble of its k, and the matching constants
+    const int prow = DX ? col >> 3 : 0;
+    const uint8_t* qw0 = smem + W_OFF + (DX ? prow * QW_ROW_BYTES : col * 4);
+    const uint8_t* sc0 = smem + W_OFF + QW_STAGE_BYTES +
+                         (DX ? (group_shift >= 7 ? 0 : (prow * 8) >> group_shift) * S_ROW_BYTES
+                             : col * 2);
+    const uint32_t byte = (uint32_t)(col & 7) >> 1;
+    const uint32_t pick = byte | byte << 4 | (byte + 4) << 8 | (byte + 4) << 12;
+    const bool high = col & 1;
+    const uint32_t nib = high ? 0x00F000F0u : 0x000F000Fu;
+    const uint32_t unit = high ? kOneSixteenth : 0x3C003C00u;  // half2(1, 1)
+    const uint32_t zero = high ? kMinus72 : 0xE408E408u;       // half2(-1032, -1032)
+
+    bool ok = true;
+    int drained = 0;  // tiles whose accumulator this warp has read out
+    for (int g = grp; g < G; g += DQ_GROUPS) {
+      // Read out every finished tile before this stage.  One must be read
+      // out first if this stage's A slot was last used by a later tile, whose
+      // MMAs wait for the accumulator.
+      const int it = g / KB;
+      while (drained < it) {
+        const bool forced = g - AS >= (drained + 1) * KB;
+        const bool done = __shfl_sync(
+            0xffffffffu, (int)mbar_test_wait(smem_u32(&bar->dfull), (uint32_t)drained & 1u), 0);
+        if (!forced && !done) break;
+        ok = drain(drained);
+        if (!ok) break;
+        ++drained;
+      }
+      if (!ok) {
+        if (lane == 0) record_timeout(err, bar);
+        break;
+      }
+      const uint32_t ph = (uint32_t)(g / DQ_GROUPS) & 1u;  // A slot phase
+      const int jw = g % WS;                                // weight slot
+      const uint32_t pw = (uint32_t)(g / WS) & 1u;
+      const uint8_t* qw = qw0 + jw * W_STAGE_BYTES;
+      const uint8_t* sc = sc0 + jw * W_STAGE_BYTES;
+      // qweight and scale tiles of the stage have landed
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_bounded<true>(&bar->wfull[jw], pw, abort_flag, kWaitLimitNs));
+      if (!ok) {
+        if (lane == 0) record_timeout(err, bar);
+        break;
+      }
+      // the stage's 128 k (or n), one half (32 TMEM columns) at a time
+      uint32_t cells[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (DX) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // eight columns n: two words' quads, one of scales
+            const uint4 wa = *reinterpret_cast<const uint4*>(qw + (64 * h + 8 * i) * 4);
+            const uint4 wb = *reinterpret_cast<const uint4*>(qw + (64 * h + 8 * i + 4) * 4);
+            const uint4 s8 = *reinterpret_cast<const uint4*>(sc + (64 * h + 8 * i) * 2);
+            const uint32_t w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+            const uint32_t s2[4] = {s8.x, s8.y, s8.z, s8.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t t = prmt(w[2 * q], w[2 * q + 1], pick);
+              // 1024 + q, or 1024 + 16 q; then q - 8 exactly; then one rounding
+              const uint32_t c = hfma2_rn(lop3_and_or(t, nib, kMagic1024), unit, zero);
+              cells[4 * i + q] = hmul2_rn(c, s2[q]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int r8 = 0; r8 < 8; ++r8) {
+            const int r = 8 * h + r8;
+            // scale row of packed row r inside the stage (0 unless the group is
+            // smaller than the 128-k stage)
+            const int gl = group_shift >= 7 ? 0 : (r * 8) >> group_shift;
+            const uint16_t sv = *reinterpret_cast<const uint16_t*>(sc + gl * S_ROW_BYTES);
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(qw + r * QW_ROW_BYTES);
+            uint32_t nat[4];
+            dequant_word_natural(w, half2_broadcast(sv), nat);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) cells[4 * r8 + q] = nat[q];
+          }
+        }
+        if (h == 0) {
+          // the A slot is free once the pair MMAs of its previous use completed
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded<true>(&bar->aempty[j], ph ^ 1u,
+                                                               abort_flag, kWaitLimitNs));
+          if (!ok) break;
+          tc_fence_after();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->wempty[jw]);  // weight tiles of the stage read
+        }
+        tmem_st_32x32b_x32(tmem + lane_addr + A_COL + j * A_STAGE_COLS + 32 * h, cells);
+      }
+      if (!ok) {
+        if (lane == 0) record_timeout(err, bar);
+        break;
+      }
+      tmem_wait_st();  // the whole warp's cells are in TMEM
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(afull_even + 8u * (uint32_t)j);
+    }
+    // the tiles not read out yet
+    while (ok && drained < NT) {
+      ok = drain(drained);
+      if (!ok && lane == 0) record_timeout(err, bar);
+      ++drained;
+    }
+    if (lane == 0) bulk_wait_all();  // this warp's stores have completed
+    __syncwarp();
+  }
+
+  // neither CTA leaves (or frees TMEM) while the pair's MMAs, loads or
+  // signals may still touch it
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+template <bool DX>
+cudaError_t launch_pair(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+                        const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
+                        int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
+  const int64_t C = DX ? N : K, O = DX ? K : N;
+  const int64_t n_groups = (group_shift == 62 || (int64_t(1) << group_shift) >= K)
+                               ? 1 : (K + (int64_t(1) << group_shift) - 1) >> group_shift;
+  const int scale_rows = group_shift >= 7 ? 1 : (BK >> group_shift);
+  XMaps x_maps;
+  CUtensorMap qw_map, s_map, y_map;
+  // X as [C/64][R][64] (one copy of both 64-column halves per stage) when C is
+  // a multiple of 64, else as [R][C] (one copy per half); rows at or beyond R
+  // and columns at or beyond C read as zero either way
+  const int x3d = C % 64 == 0;
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t rows = 32u << i;
+    const uint64_t dims[3] = {64, (uint64_t)R, (uint64_t)(C / 64)};
+    const uint64_t strides[2] = {(uint64_t)C * 2, 128};
+    const uint32_t box[3] = {64, rows, 2};
+    if (!(x3d ? encode_map_3d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_128B)
+              : encode_map_2d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)C,
+                              (uint64_t)R, (uint64_t)C * 2, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B)))
+      return cudaErrorInvalidValue;
+  }
+  const uint64_t qdims[3] = {(uint64_t)N, (uint64_t)(K / 8), (uint64_t)E};
+  const uint64_t qstrides[2] = {(uint64_t)N * 4, (uint64_t)(K / 8) * N * 4};
+  const uint32_t qbox[3] = {BW, BK / 8, 1};
+  const uint64_t sdims[3] = {(uint64_t)N, (uint64_t)n_groups, (uint64_t)E};
+  const uint64_t sstrides[2] = {(uint64_t)N * 2, (uint64_t)n_groups * N * 2};
+  const uint32_t sbox[3] = {BW, (uint32_t)scale_rows, 1};
+  if (!encode_map_3d(&qw_map, qweight, CU_TENSOR_MAP_DATA_TYPE_INT32, qdims, qstrides, qbox,
+                     CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_map_3d(&s_map, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, sdims, sstrides, sbox,
+                     CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      // Y blocks of 32 columns x 64 tokens, one per dequantisation warp
+      !encode_map_2d(&y_map, y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)O, (uint64_t)R,
+                     (uint64_t)O * 2, 32, TPG, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  static std::once_flag attr_once[64];
+  static cudaError_t attr_err[64];
+  const int d = dev.device & 63;
+  std::call_once(attr_once[d], [&] {
+    attr_err[d] = cudaFuncSetAttribute(experts_pair_kernel<DX>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       1024 + TABLE_OFF + Table::bytes(GPTQ_MOE_MAX_EXPERTS));
+  });
+  if (attr_err[d] != cudaSuccess) return attr_err[d];
+  // column pairs of 2 x 128 (with an odd count of 128-column tiles the last
+  // pair's odd CTA has no columns: it loads no weights and stores nothing);
+  // at most one token tile per row, and fewer than one per 64 rows beyond one
+  // per expert
+  const int64_t n_pairs = ((O + BW - 1) / BW + 1) / 2;
+  const int64_t tiles = n_pairs * std::min<int64_t>(R, E + R / 64);
+  const int64_t clusters = std::min<int64_t>(tiles, std::max(1, dev.num_sms / 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = 1024 + TABLE_OFF + Table::bytes((int)E);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, experts_pair_kernel<DX>, x_maps, qw_map, s_map, y_map, offsets,
+                            (int)R, (int)C, (int)O, (int)E, group_shift, scale_rows, x3d,
+                            (int)n_pairs, y, dev.error_word);
+}
+
+}  // namespace
+
+cudaError_t launch_experts_pair(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+                                const int32_t* offsets, uint16_t* y, int64_t R, int64_t K,
+                                int64_t N, int64_t E, int group_shift, cudaStream_t stream,
+                                const DeviceInfo& dev) {
+  return launch_pair<false>(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
+}
+
+cudaError_t launch_experts_dx(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales,
+                              const int32_t* offsets, uint16_t* dx, int64_t R, int64_t K,
+                              int64_t N, int64_t E, int group_shift, cudaStream_t stream,
+                              const DeviceInfo& dev) {
+  return launch_pair<true>(dy, qweight, scales, offsets, dx, R, K, N, E, group_shift, stream,
+                           dev);
+}
+
+}  // namespace gptq

@@ -25,7 +25,7 @@ constexpr int kTFlagSlots = 1024;
 
 // Error codes written to the device error word (match gptq_status values).
 constexpr int kDeviceErrTimeout = 7;
-constexpr int kDeviceErrIndex = 10;  // a g_idx entry outside 0 .. n_groups - 1
+constexpr int kDeviceErrIndex = 10;  // a g_idx entry, expert offset or place out of range
 
 // log2(group), or 62 for group == -1 (then (8*i) >> 62 == 0 for every row).
 inline int group_shift_of(int32_t group) {
@@ -115,6 +115,27 @@ cudaError_t launch_prefill_pair_asym(const uint16_t* x, const int32_t* qweight,
 cudaError_t launch_lora_down(const uint16_t* x, const uint16_t* lora_a, uint16_t* t, int64_t M,
                              int64_t K, int64_t r, int free_sms, cudaStream_t stream,
                              const DeviceInfo& dev);
+// Mixture-of-experts token movement (moe.cu).  id_bytes: 4 or 8.
+cudaError_t launch_moe_sort(const uint16_t* x, const void* ids, int id_bytes, int64_t M,
+                            int64_t H, int topk, int E, uint16_t* x_sorted, int32_t* offsets,
+                            int32_t* dest, cudaStream_t stream, const DeviceInfo& dev);
+cudaError_t launch_moe_combine(const uint16_t* y, const int32_t* dest, const float* weights,
+                               int64_t M, int64_t H, int topk, int64_t R, uint16_t* out,
+                               cudaStream_t stream, const DeviceInfo& dev);
+cudaError_t launch_moe_combine_backward(const uint16_t* dout, const uint16_t* y,
+                                        const int32_t* dest, const float* weights, int64_t M,
+                                        int64_t H, int topk, int64_t R, uint16_t* dy, float* dw,
+                                        cudaStream_t stream, const DeviceInfo& dev);
+// The experts' products on CTA pairs (experts_pair.cu), and the gradient with
+// respect to their rows.
+cudaError_t launch_experts_pair(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+                                const int32_t* offsets, uint16_t* y, int64_t R, int64_t K,
+                                int64_t N, int64_t E, int group_shift, cudaStream_t stream,
+                                const DeviceInfo& dev);
+cudaError_t launch_experts_dx(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales,
+                              const int32_t* offsets, uint16_t* dx, int64_t R, int64_t K,
+                              int64_t N, int64_t E, int group_shift, cudaStream_t stream,
+                              const DeviceInfo& dev);
 // CTAs of one decode launch of this shape (column blocks x K split).
 int64_t decode_ctas(int64_t M, int64_t K, int64_t N, bool lora, const DeviceInfo& dev);
 

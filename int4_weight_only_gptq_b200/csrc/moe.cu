@@ -1,0 +1,508 @@
+// Token movement of a mixture-of-experts layer: tokens sorted by expert, the
+// experts' rows combined back into tokens, and the gradients of both.
+//
+// With expert ids e(m, j) (token m's j-th choice, pair p = m * topk + j) and
+// the stable order of the pairs by expert,
+//   dest[p]   = #{q : e(q) < e(p)} + #{q < p : e(q) = e(p)}   (-1 if dropped)
+//   x_sorted[dest[p]] = x[m]
+//   out[m]    = sum_j w[p] * y_sorted[dest[p]]
+//   dy_sorted[dest[p]] = w[p] * dout[m],  dw[p] = <dout[m], y_sorted[dest[p]]>
+// and the gradient of x is the weightless sum of its rows' gradients, which is
+// the combine with w = 1.  All of it is bound by memory traffic (or, for a few
+// tokens, by launch latency): rows move in 16-byte chunks, each input row is
+// read once, sums are FP32 in a fixed order (bitwise reproducible), and every
+// result is rounded once.  No kernel uses atomics on data it returns.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "gptq_w4a16.h"
+#include "kernels.h"
+
+namespace gptq {
+
+namespace {
+
+__device__ __forceinline__ void wait_previous_grid() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void let_next_grid_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Streaming 16-byte load on the coherent path: these grids may start while the
+// previous one still runs, so nothing it writes is read as read-only data
+// (for the same reason the kernels' pointers carry no __restrict__).
+__device__ __forceinline__ uint4 ld_row_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ float2 half2_to_float2(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+__device__ __forceinline__ uint32_t floats_to_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The expert of a pair, or E if the id names no expert (the pair is dropped).
+template <typename Id>
+__device__ __forceinline__ int key_of(const Id* ids, int64_t p, int E) {
+  const Id v = ids[p];
+  return v >= 0 && v < (Id)E ? (int)v : E;
+}
+
+// ---- sort, few pairs: one launch ------------------------------------------
+//
+// Every CTA holds all keys in shared memory and counts the places of its own
+// tokens' pairs directly from the definition of dest: O(pairs) work per pair,
+// which for up to kSortSmallPairs pairs takes less time than a second launch.
+// The last CTA writes the experts' offsets (a histogram and a scan).
+constexpr int kSortSmallPairs = 4096;
+constexpr int kSmallThreads = 256;
+constexpr int kSmallWarps = kSmallThreads / 32;
+
+template <typename Id>
+__global__ void __launch_bounds__(kSmallThreads)
+    sort_small_kernel(const uint16_t* x, const Id* ids, int M, int H,
+                      int topk, int E, uint16_t* x_sorted,
+                      int32_t* offsets, int32_t* dest) {
+  extern __shared__ int keys[];
+  __shared__ int places[GPTQ_MOE_MAX_TOPK];
+  __shared__ int counts[GPTQ_MOE_MAX_EXPERTS];
+  wait_previous_grid();
+  let_next_grid_start();
+  const int P = M * topk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int p = threadIdx.x; p < P; p += kSmallThreads) keys[p] = key_of(ids, p, E);
+  if ((int)blockIdx.x == gridDim.x - 1) {
+    for (int e = threadIdx.x; e < E; e += kSmallThreads) counts[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < P; p += kSmallThreads)
+      if (keys[p] < E) atomicAdd(&counts[keys[p]], 1);
+    __syncthreads();
+    if (warp == 0) {
+      int before = 0;
+      for (int e0 = 0; e0 < E; e0 += 32) {
+        const int c = e0 + lane < E ? counts[e0 + lane] : 0;
+        int s = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += v;
+        }
+        if (e0 + lane < E) offsets[e0 + lane] = before + s - c;
+        before += __shfl_sync(0xffffffffu, s, 31);
+      }
+      if (lane == 0) offsets[E] = before;
+    }
+    return;
+  }
+  __syncthreads();
+  for (int m = blockIdx.x; m < M; m += gridDim.x - 1) {
+    for (int j = warp; j < topk; j += kSmallWarps) {
+      const int p = m * topk + j, e = keys[p];
+      int n = 0;
+      if (e < E) {
+        for (int q = lane; q < P; q += 32) {
+          const int k = keys[q];
+          n += (k < e || (k == e && q < p)) ? 1 : 0;
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+      } else {
+        n = -1;
+      }
+      if (lane == 0) {
+        places[j] = n;
+        dest[p] = n;
+      }
+    }
+    __syncthreads();
+    const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)m * H);
+    for (int c = threadIdx.x; c < H / 8; c += kSmallThreads) {
+      const uint4 v = src[c];
+      for (int j = 0; j < topk; ++j)
+        if (places[j] >= 0)
+          reinterpret_cast<uint4*>(x_sorted + (int64_t)places[j] * H)[c] = v;
+    }
+    __syncthreads();
+  }
+}
+
+// ---- sort, many pairs: places by one cluster, then the rows ------------------
+//
+// One cluster of eight CTAs; every warp owns a contiguous run of pairs and
+// walks it twice: once counting its pairs per expert (lanes with equal keys
+// found by a warp match; the first of them adds their number), once handing
+// out places from its running base per expert.  Between the walks the counts
+// are turned into bases: over the warps of a CTA, over the CTAs (distributed
+// shared memory), over the experts.  The order of pairs is kept throughout, so
+// the sort is stable and needs no atomics and no scratch memory.
+constexpr int kPlaceCtas = 8;
+constexpr int kPlaceThreads = 1024;
+constexpr int kPlaceWarps = kPlaceThreads / 32;
+
+constexpr size_t place_smem_bytes(int E) { return ((size_t)kPlaceWarps + 2) * E * sizeof(int); }
+
+__device__ __forceinline__ int ld_dsmem_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename Id>
+__global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThreads)
+    sort_place_kernel(const Id* ids, int64_t P, int E,
+                      int32_t* offsets, int32_t* dest) {
+  // warp w's count, then base, of expert e: base[w * E + e]; this CTA's total
+  // of expert e: total[e]; the first place of expert e: first[e]
+  extern __shared__ int sm[];
+  int* base = sm;
+  int* total = sm + kPlaceWarps * E;
+  int* first = total + E;
+  __shared__ int warp_sums[kPlaceWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = (int)cluster_ctarank();
+  wait_previous_grid();
+  let_next_grid_start();
+  const int64_t w = (int64_t)cta * kPlaceWarps + warp;
+  constexpr int64_t W = kPlaceCtas * kPlaceWarps;
+  const int64_t begin = P * w / W, end = P * (w + 1) / W;
+  int* mine = base + warp * E;
+  for (int e = lane; e < E; e += 32) mine[e] = 0;
+  __syncwarp();
+  for (int64_t p0 = begin; p0 < end; p0 += 32) {
+    const int64_t p = p0 + lane;
+    const int key = p < end ? key_of(ids, p, E) : E;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    if (key < E && (same & ((1u << lane) - 1u)) == 0) mine[key] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kPlaceThreads) {
+    int sum = 0;
+    for (int v = 0; v < kPlaceWarps; ++v) {
+      const int c = base[v * E + e];
+      base[v * E + e] = sum;
+      sum += c;
+    }
+    total[e] = sum;
+  }
+  cluster_sync_all();
+  // thread e (E <= 1024 threads): this expert's pairs in all CTAs and in the
+  // CTAs before this one, then the scan over the experts
+  int before = 0, all = 0;
+  if ((int)threadIdx.x < E) {
+    for (int c = 0; c < kPlaceCtas; ++c) {
+      const int n = ld_dsmem_s32(map_to_rank(smem_u32(&total[threadIdx.x]), (uint32_t)c));
+      if (c < cta) before += n;
+      all += n;
+    }
+  }
+  int scan = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) warp_sums[warp] = scan;
+  __syncthreads();
+  int prior = 0;
+  for (int v = 0; v < warp; ++v) prior += warp_sums[v];
+  const int start = prior + scan - all;  // the expert's first row
+  if ((int)threadIdx.x < E) {
+    first[threadIdx.x] = start + before;
+    if (cta == 0) {
+      offsets[threadIdx.x] = start;
+      if ((int)threadIdx.x == E - 1) offsets[E] = start + all;
+    }
+  }
+  // no CTA leaves while another may still read its totals
+  cluster_sync_all();
+  for (int e = lane; e < E; e += 32) mine[e] += first[e];
+  __syncwarp();
+  for (int64_t p0 = begin; p0 < end; p0 += 32) {
+    const int64_t p = p0 + lane;
+    const int key = p < end ? key_of(ids, p, E) : E;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const int lower = __popc(same & ((1u << lane) - 1u));
+    const int at = key < E ? mine[key] : 0;
+    __syncwarp();
+    if (key < E && lower == 0) mine[key] = at + __popc(same);
+    __syncwarp();
+    if (p < end) dest[p] = key < E ? at + lower : -1;
+  }
+}
+
+// Rows: a warp takes 1024 values (four 16-byte chunks per lane) of one token,
+// reads them once and writes them to each of the token's places.
+constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kGatherChunks = 4;
+
+__global__ void __launch_bounds__(kRowThreads)
+    sort_rows_kernel(const uint16_t* x, const int32_t* dest, int64_t M, int H,
+                     int topk, int segments, uint16_t* x_sorted) {
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  wait_previous_grid();
+  let_next_grid_start();
+  const int64_t m = unit / segments;
+  if (m >= M) return;
+  const int c0 = (int)(unit - m * segments) * (32 * kGatherChunks) + lane, chunks = H / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(x + m * H);
+  uint4 v[kGatherChunks];
+#pragma unroll
+  for (int i = 0; i < kGatherChunks; ++i)
+    if (c0 + 32 * i < chunks) v[i] = ld_row_v4(src + c0 + 32 * i);
+  for (int j0 = 0; j0 < topk; j0 += 32) {
+    const int mine = j0 + lane < topk ? dest[m * topk + j0 + lane] : -1;
+    const int n = min(32, topk - j0);
+    for (int j = 0; j < n; ++j) {
+      const int d = __shfl_sync(0xffffffffu, mine, j);
+      if (d < 0) continue;
+      uint4* out = reinterpret_cast<uint4*>(x_sorted + (int64_t)d * H);
+#pragma unroll
+      for (int i = 0; i < kGatherChunks; ++i)
+        if (c0 + 32 * i < chunks) out[c0 + 32 * i] = v[i];
+    }
+  }
+}
+
+// ---- combine -----------------------------------------------------------------
+
+// A place read from dest: -1 if the pair was dropped; one outside the rows is
+// reported and treated as dropped.
+__device__ __forceinline__ int checked_place(int d, int64_t R, int* err) {
+  if (d >= R) {
+    atomicCAS(err, 0, kDeviceErrIndex);
+    return -1;
+  }
+  return d < 0 ? -1 : d;
+}
+
+// A warp takes 512 values (two chunks per lane) of one token and adds its
+// rows in the order of the choices, FP32, four rows' loads in flight.
+constexpr int kCombineChunks = 2;
+constexpr int kCombineAhead = 4;
+
+template <bool WEIGHTED>
+__global__ void __launch_bounds__(kRowThreads)
+    combine_kernel(const uint16_t* y, const int32_t* dest,
+                   const float* weights, int64_t M, int H, int topk, int64_t R,
+                   int segments, uint16_t* out, int* err) {
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  wait_previous_grid();
+  let_next_grid_start();
+  const int64_t m = unit / segments;
+  if (m >= M) return;
+  const int c0 = (int)(unit - m * segments) * (32 * kCombineChunks) + lane, chunks = H / 8;
+  float acc[kCombineChunks][8];
+#pragma unroll
+  for (int i = 0; i < kCombineChunks; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[i][q] = 0.f;
+  for (int j0 = 0; j0 < topk; j0 += 32) {
+    const int n = min(32, topk - j0);
+    const int64_t p = m * topk + j0 + lane;
+    const int place = lane < n ? checked_place(dest[p], R, err) : -1;
+    const float weight = WEIGHTED && lane < n ? weights[p] : 1.f;
+    for (int j = 0; j < n; j += kCombineAhead) {
+      uint4 v[kCombineAhead][kCombineChunks];
+      int d[kCombineAhead];
+#pragma unroll
+      for (int a = 0; a < kCombineAhead; ++a) {
+        d[a] = j + a < n ? __shfl_sync(0xffffffffu, place, j + a) : -1;
+        const uint4* src = reinterpret_cast<const uint4*>(y + (int64_t)d[a] * H);
+#pragma unroll
+        for (int i = 0; i < kCombineChunks; ++i)
+          if (d[a] >= 0 && c0 + 32 * i < chunks) v[a][i] = ld_row_v4(src + c0 + 32 * i);
+      }
+#pragma unroll
+      for (int a = 0; a < kCombineAhead; ++a) {
+        if (d[a] < 0) continue;  // the same for the whole warp
+        const float w = __shfl_sync(0xffffffffu, weight, j + a);
+#pragma unroll
+        for (int i = 0; i < kCombineChunks; ++i) {
+          const uint32_t h[4] = {v[a][i].x, v[a][i].y, v[a][i].z, v[a][i].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = half2_to_float2(h[q]);
+            acc[i][2 * q] = fmaf(w, f.x, acc[i][2 * q]);
+            acc[i][2 * q + 1] = fmaf(w, f.y, acc[i][2 * q + 1]);
+          }
+        }
+      }
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(out + m * H);
+#pragma unroll
+  for (int i = 0; i < kCombineChunks; ++i)
+    if (c0 + 32 * i < chunks)
+      dst[c0 + 32 * i] = make_uint4(floats_to_half2(acc[i][0], acc[i][1]),
+                                    floats_to_half2(acc[i][2], acc[i][3]),
+                                    floats_to_half2(acc[i][4], acc[i][5]),
+                                    floats_to_half2(acc[i][6], acc[i][7]));
+}
+
+// ---- combine, backward ---------------------------------------------------------
+
+// One CTA per token, eight choices at a time: each thread keeps its chunks of
+// dout, reads the rows' chunks, stores w * dout (one rounding) and adds up its
+// part of the eight dot products; lanes by shuffles, warps in order.
+constexpr int kBackThreads = 128;
+constexpr int kBackWarps = kBackThreads / 32;
+constexpr int kBackChoices = 8;
+
+__global__ void __launch_bounds__(kBackThreads)
+    combine_backward_kernel(const uint16_t* dout, const uint16_t* y,
+                            const int32_t* dest, const float* weights,
+                            int H, int topk, int64_t R, uint16_t* dy,
+                            float* dw, int* err) {
+  __shared__ float part[kBackWarps][kBackChoices];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  wait_previous_grid();
+  let_next_grid_start();
+  const int64_t m = blockIdx.x;
+  const int chunks = H / 8;
+  const uint4* g = reinterpret_cast<const uint4*>(dout + m * H);
+  for (int j0 = 0; j0 < topk; j0 += kBackChoices) {
+    int d[kBackChoices];
+    float w[kBackChoices], dot[kBackChoices];
+#pragma unroll
+    for (int j = 0; j < kBackChoices; ++j) {
+      const int64_t p = m * topk + j0 + j;
+      d[j] = j0 + j < topk ? checked_place(dest[p], R, err) : -1;
+      w[j] = j0 + j < topk ? weights[p] : 0.f;
+      dot[j] = 0.f;
+    }
+    for (int c = threadIdx.x; c < chunks; c += kBackThreads) {
+      const uint4 gv = g[c];
+      uint4 v[kBackChoices];
+#pragma unroll
+      for (int j = 0; j < kBackChoices; ++j)
+        if (d[j] >= 0)
+          v[j] = ld_row_v4(reinterpret_cast<const uint4*>(y + (int64_t)d[j] * H) + c);
+      const float2 g0 = half2_to_float2(gv.x), g1 = half2_to_float2(gv.y);
+      const float2 g2 = half2_to_float2(gv.z), g3 = half2_to_float2(gv.w);
+#pragma unroll
+      for (int j = 0; j < kBackChoices; ++j) {
+        if (d[j] < 0) continue;
+        fma8(dot[j], v[j], g0, g1, g2, g3);
+        reinterpret_cast<uint4*>(dy + (int64_t)d[j] * H)[c] =
+            make_uint4(floats_to_half2(w[j] * g0.x, w[j] * g0.y),
+                       floats_to_half2(w[j] * g1.x, w[j] * g1.y),
+                       floats_to_half2(w[j] * g2.x, w[j] * g2.y),
+                       floats_to_half2(w[j] * g3.x, w[j] * g3.y));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBackChoices; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_down_sync(0xffffffffu, dot[j], o);
+      if (lane == 0) part[warp][j] = dot[j];
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < kBackChoices && j0 + (int)threadIdx.x < topk) {
+      float s = 0.f;
+      for (int v = 0; v < kBackWarps; ++v) s += part[v][threadIdx.x];
+      dw[m * topk + j0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// A launch that may begin while the previous kernel of the stream ends: every
+// kernel above waits for it before it reads or writes anything.
+struct Launch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  Launch(int64_t grid, int block, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+template <typename Id>
+cudaError_t launch_sort(const uint16_t* x, const Id* ids, int64_t M, int64_t H, int topk, int E,
+                        uint16_t* x_sorted, int32_t* offsets, int32_t* dest, cudaStream_t stream,
+                        const DeviceInfo& dev) {
+  const int64_t P = M * topk;
+  if (P <= kSortSmallPairs) {
+    // one CTA per token up to eight per SM, and the one that writes offsets
+    const int64_t ctas = std::min<int64_t>(M, 8 * (int64_t)dev.num_sms) + 1;
+    const Launch l(ctas, kSmallThreads, (size_t)P * sizeof(int), stream);
+    return cudaLaunchKernelEx(&l.cfg, sort_small_kernel<Id>, x, ids, (int)M, (int)H, topk, E,
+                              x_sorted, offsets, dest);
+  }
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  const int di = dev.device & 63;
+  std::call_once(once[di], [&] {
+    attr_err[di] = cudaFuncSetAttribute(sort_place_kernel<Id>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)place_smem_bytes(GPTQ_MOE_MAX_EXPERTS));
+  });
+  if (attr_err[di] != cudaSuccess) return attr_err[di];
+  const size_t smem = place_smem_bytes(E);
+  cudaError_t e;
+  const Launch place(kPlaceCtas, kPlaceThreads, smem, stream);
+  e = cudaLaunchKernelEx(&place.cfg, sort_place_kernel<Id>, ids, P, E, offsets, dest);
+  if (e != cudaSuccess) return e;
+  const int segments = (int)((H / 8 + 32 * kGatherChunks - 1) / (32 * kGatherChunks));
+  const int64_t units = M * segments;
+  const Launch rows((units + kRowWarps - 1) / kRowWarps, kRowThreads, 0, stream);
+  return cudaLaunchKernelEx(&rows.cfg, sort_rows_kernel, x, (const int32_t*)dest, M, (int)H, topk,
+                            segments, x_sorted);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_sort(const uint16_t* x, const void* ids, int id_bytes, int64_t M,
+                            int64_t H, int topk, int E, uint16_t* x_sorted, int32_t* offsets,
+                            int32_t* dest, cudaStream_t stream, const DeviceInfo& dev) {
+  if (id_bytes == 8)
+    return launch_sort(x, static_cast<const int64_t*>(ids), M, H, topk, E, x_sorted, offsets,
+                       dest, stream, dev);
+  return launch_sort(x, static_cast<const int32_t*>(ids), M, H, topk, E, x_sorted, offsets, dest,
+                     stream, dev);
+}
+
+cudaError_t launch_moe_combine(const uint16_t* y, const int32_t* dest, const float* weights,
+                               int64_t M, int64_t H, int topk, int64_t R, uint16_t* out,
+                               cudaStream_t stream, const DeviceInfo& dev) {
+  const int segments = (int)((H / 8 + 32 * kCombineChunks - 1) / (32 * kCombineChunks));
+  const int64_t units = M * segments;
+  // few tokens: one warp per CTA, so that their loads spread over the SMs
+  const int warps = units < 8 * (int64_t)dev.num_sms ? 1 : kRowWarps;
+  const Launch l((units + warps - 1) / warps, 32 * warps, 0, stream);
+  return weights ? cudaLaunchKernelEx(&l.cfg, combine_kernel<true>, y, dest, weights, M, (int)H,
+                                      topk, R, segments, out, dev.error_word)
+                 : cudaLaunchKernelEx(&l.cfg, combine_kernel<false>, y, dest, weights, M, (int)H,
+                                      topk, R, segments, out, dev.error_word);
+}
+
+cudaError_t launch_moe_combine_backward(const uint16_t* dout, const uint16_t* y,
+                                        const int32_t* dest, const float* weights, int64_t M,
+                                        int64_t H, int topk, int64_t R, uint16_t* dy, float* dw,
+                                        cudaStream_t stream, const DeviceInfo& dev) {
+  const Launch l(M, kBackThreads, 0, stream);
+  return cudaLaunchKernelEx(&l.cfg, combine_backward_kernel, dout, y, dest, weights, (int)H, topk,
+                            R, dy, dw, dev.error_word);
+}
+
+}  // namespace gptq

@@ -64,13 +64,7 @@ uint64_t hash(const Key& k) {
   return h ^ (h >> 29);
 }
 
-bool encode_cached(CUtensorMap* out, const Key& key) {
-  thread_local Entry cache[kSlots];
-  Entry& e = cache[hash(key) % kSlots];
-  if (e.valid && e.key == key) {
-    *out = e.map;
-    return true;
-  }
+bool encode_key(CUtensorMap* out, const Key& key) {
   EncodeTiledFn encode = encode_fn();
   if (!encode) return false;
   cuuint64_t gdim[3], gstride[2];
@@ -81,12 +75,22 @@ bool encode_cached(CUtensorMap* out, const Key& key) {
     estride[i] = 1;
   }
   for (int i = 0; i + 1 < key.rank; ++i) gstride[i] = key.stride[i];
+  return encode(out, (CUtensorMapDataType)key.dtype, (cuuint32_t)key.rank,
+                const_cast<void*>(key.ptr), gdim, gstride, box, estride,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, (CUtensorMapSwizzle)key.swizzle,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_cached(CUtensorMap* out, const Key& key) {
+  thread_local Entry cache[kSlots];
+  Entry& e = cache[hash(key) % kSlots];
+  if (e.valid && e.key == key) {
+    *out = e.map;
+    return true;
+  }
   CUtensorMap map;
-  if (encode(&map, (CUtensorMapDataType)key.dtype, (cuuint32_t)key.rank, const_cast<void*>(key.ptr),
-             gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             (CUtensorMapSwizzle)key.swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
+  if (!encode_key(&map, key)) return false;
   e.valid = true;
   e.key = key;
   e.map = map;
@@ -109,6 +113,21 @@ bool tensor_map_3d(CUtensorMap* out, const void* ptr, CUtensorMapDataType dtype,
   const Key key{ptr, 3, (int)dtype, (int)swizzle, {dims[0], dims[1], dims[2]},
                 {strides[0], strides[1]}, {box[0], box[1], box[2]}};
   return encode_cached(out, key);
+}
+
+bool encode_map_2d(CUtensorMap* out, const void* ptr, CUtensorMapDataType dtype, uint64_t dim0,
+                   uint64_t dim1, uint64_t row_bytes, uint32_t box0, uint32_t box1,
+                   CUtensorMapSwizzle swizzle) {
+  const Key key{ptr, 2, (int)dtype, (int)swizzle, {dim0, dim1, 1}, {row_bytes, 0}, {box0, box1, 1}};
+  return encode_key(out, key);
+}
+
+bool encode_map_3d(CUtensorMap* out, const void* ptr, CUtensorMapDataType dtype,
+                   const uint64_t dims[3], const uint64_t strides[2], const uint32_t box[3],
+                   CUtensorMapSwizzle swizzle) {
+  const Key key{ptr, 3, (int)dtype, (int)swizzle, {dims[0], dims[1], dims[2]},
+                {strides[0], strides[1]}, {box[0], box[1], box[2]}};
+  return encode_key(out, key);
 }
 
 }  // namespace gptq

@@ -20,4 +20,14 @@ bool tensor_map_3d(CUtensorMap* out, const void* ptr, CUtensorMapDataType dtype,
                    const uint64_t dims[3], const uint64_t strides[2], const uint32_t box[3],
                    CUtensorMapSwizzle swizzle);
 
+// The same, encoded anew on every call: for buffers that a caller allocates
+// per call (an activation's rows), which would only push others out of the
+// cache.
+bool encode_map_2d(CUtensorMap* out, const void* ptr, CUtensorMapDataType dtype, uint64_t dim0,
+                   uint64_t dim1, uint64_t row_bytes, uint32_t box0, uint32_t box1,
+                   CUtensorMapSwizzle swizzle);
+bool encode_map_3d(CUtensorMap* out, const void* ptr, CUtensorMapDataType dtype,
+                   const uint64_t dims[3], const uint64_t strides[2], const uint32_t box[3],
+                   CUtensorMapSwizzle swizzle);
+
 }  // namespace gptq
