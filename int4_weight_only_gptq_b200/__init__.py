@@ -11,7 +11,8 @@ __version__ = "0.1.0"
 
 _BINDING_NAMES = {"gemm", "gemm_grouped", "gemm_asym", "gemm_gidx", "gemm_lora",
                   "gemm_lora_noalloc", "moe_sort", "moe_combine", "moe_combine_backward",
-                  "gemm_experts", "gemm_experts_dx", "dequant", "select", "device_error", "version", "load",
+                  "gemm_experts", "gemm_experts_dx", "dequant", "select", "device_error",
+                  "version", "load",
                   "GptqError", "KERNEL_AUTO", "KERNEL_DECODE", "KERNEL_PREFILL", "DECODE_MAX_M",
                   "LORA_DECODE_MAX_M", "MAX_GROUPED", "MAX_LORA_RANK", "LORA_SCRATCH_BYTES",
                   "GIDX_MAX_GROUPS", "MOE_MAX_EXPERTS", "MOE_MAX_TOPK", "GROUP_SIZES"}
@@ -20,5 +21,7 @@ _BINDING_NAMES = {"gemm", "gemm_grouped", "gemm_asym", "gemm_gidx", "gemm_lora",
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        # kept, so that later uses are plain attribute lookups
+        value = globals()[name] = getattr(binding, name)
+        return value
     raise AttributeError(name)

@@ -381,34 +381,30 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
 
 
 def _require_moe(t, name: str, dtype, device, shape=None):
-    """The checks of _require and _check_shape in one pass: the token movement
-    calls last a few microseconds on the device, so their checks are kept
-    short."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (row-major)")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}")
-    if shape is not None and t.shape != shape:
+    """The checks of _require and _check_shape in one pass: the calls of a
+    decoding step last a few microseconds on the device, so their checks are
+    kept short."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
+            and t.device == device and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        _require(t, name, lambda d: d == dtype, device)
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        # the handle of torch.cuda.current_stream(device), without the object
+        stream = torch._C._cuda_getCurrentRawStream(device.index)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status != 0:
+        _check(status)
 
 
 def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,

@@ -355,63 +355,75 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // ---- combine, backward ---------------------------------------------------------
 
-// One CTA per token, eight choices at a time: each thread keeps its chunks of
-// dout, reads the rows' chunks, stores w * dout (one rounding) and adds up its
-// part of the eight dot products; lanes by shuffles, warps in order.
+// One CTA per token, CHOICES choices at a time: each thread takes AHEAD chunks
+// of dout and the rows' chunks beside them (all loads in flight together),
+// stores w * dout (one rounding) and adds up its part of the dot products;
+// lanes by shuffles, warps in order.  CHOICES * AHEAD = 8 keeps the loads in
+// flight, and with them the bandwidth, the same for few choices as for many:
+// two choices of 8192 x 5120 took 101 us with AHEAD = 1 (4.2 TB/s).
 constexpr int kBackThreads = 128;
 constexpr int kBackWarps = kBackThreads / 32;
-constexpr int kBackChoices = 8;
 
+template <int CHOICES, int AHEAD>
 __global__ void __launch_bounds__(kBackThreads)
-    combine_backward_kernel(const uint16_t* dout, const uint16_t* y,
-                            const int32_t* dest, const float* weights,
-                            int H, int topk, int64_t R, uint16_t* dy,
+    combine_backward_kernel(const uint16_t* dout, const uint16_t* y, const int32_t* dest,
+                            const float* weights, int H, int topk, int64_t R, uint16_t* dy,
                             float* dw, int* err) {
-  __shared__ float part[kBackWarps][kBackChoices];
+  __shared__ float part[kBackWarps][CHOICES];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   wait_previous_grid();
   let_next_grid_start();
   const int64_t m = blockIdx.x;
   const int chunks = H / 8;
   const uint4* g = reinterpret_cast<const uint4*>(dout + m * H);
-  for (int j0 = 0; j0 < topk; j0 += kBackChoices) {
-    int d[kBackChoices];
-    float w[kBackChoices], dot[kBackChoices];
+  for (int j0 = 0; j0 < topk; j0 += CHOICES) {
+    int d[CHOICES];
+    float w[CHOICES], dot[CHOICES];
 #pragma unroll
-    for (int j = 0; j < kBackChoices; ++j) {
+    for (int j = 0; j < CHOICES; ++j) {
       const int64_t p = m * topk + j0 + j;
       d[j] = j0 + j < topk ? checked_place(dest[p], R, err) : -1;
       w[j] = j0 + j < topk ? weights[p] : 0.f;
       dot[j] = 0.f;
     }
-    for (int c = threadIdx.x; c < chunks; c += kBackThreads) {
-      const uint4 gv = g[c];
-      uint4 v[kBackChoices];
+    for (int c0 = threadIdx.x; c0 < chunks; c0 += kBackThreads * AHEAD) {
+      uint4 gv[AHEAD], v[AHEAD][CHOICES];
 #pragma unroll
-      for (int j = 0; j < kBackChoices; ++j)
-        if (d[j] >= 0)
-          v[j] = ld_row_v4(reinterpret_cast<const uint4*>(y + (int64_t)d[j] * H) + c);
-      const float2 g0 = half2_to_float2(gv.x), g1 = half2_to_float2(gv.y);
-      const float2 g2 = half2_to_float2(gv.z), g3 = half2_to_float2(gv.w);
+      for (int a = 0; a < AHEAD; ++a) {
+        const int c = c0 + a * kBackThreads;
+        if (c >= chunks) break;
+        gv[a] = ld_row_v4(g + c);
 #pragma unroll
-      for (int j = 0; j < kBackChoices; ++j) {
-        if (d[j] < 0) continue;
-        fma8(dot[j], v[j], g0, g1, g2, g3);
-        reinterpret_cast<uint4*>(dy + (int64_t)d[j] * H)[c] =
-            make_uint4(floats_to_half2(w[j] * g0.x, w[j] * g0.y),
-                       floats_to_half2(w[j] * g1.x, w[j] * g1.y),
-                       floats_to_half2(w[j] * g2.x, w[j] * g2.y),
-                       floats_to_half2(w[j] * g3.x, w[j] * g3.y));
+        for (int j = 0; j < CHOICES; ++j)
+          if (d[j] >= 0)
+            v[a][j] = ld_row_v4(reinterpret_cast<const uint4*>(y + (int64_t)d[j] * H) + c);
+      }
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int c = c0 + a * kBackThreads;
+        if (c >= chunks) break;
+        const float2 g0 = half2_to_float2(gv[a].x), g1 = half2_to_float2(gv[a].y);
+        const float2 g2 = half2_to_float2(gv[a].z), g3 = half2_to_float2(gv[a].w);
+#pragma unroll
+        for (int j = 0; j < CHOICES; ++j) {
+          if (d[j] < 0) continue;
+          fma8(dot[j], v[a][j], g0, g1, g2, g3);
+          reinterpret_cast<uint4*>(dy + (int64_t)d[j] * H)[c] =
+              make_uint4(floats_to_half2(w[j] * g0.x, w[j] * g0.y),
+                         floats_to_half2(w[j] * g1.x, w[j] * g1.y),
+                         floats_to_half2(w[j] * g2.x, w[j] * g2.y),
+                         floats_to_half2(w[j] * g3.x, w[j] * g3.y));
+        }
       }
     }
 #pragma unroll
-    for (int j = 0; j < kBackChoices; ++j) {
+    for (int j = 0; j < CHOICES; ++j) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_down_sync(0xffffffffu, dot[j], o);
       if (lane == 0) part[warp][j] = dot[j];
     }
     __syncthreads();
-    if ((int)threadIdx.x < kBackChoices && j0 + (int)threadIdx.x < topk) {
+    if ((int)threadIdx.x < CHOICES && j0 + (int)threadIdx.x < topk) {
       float s = 0.f;
       for (int v = 0; v < kBackWarps; ++v) s += part[v][threadIdx.x];
       dw[m * topk + j0 + threadIdx.x] = s;
@@ -501,8 +513,12 @@ cudaError_t launch_moe_combine_backward(const uint16_t* dout, const uint16_t* y,
                                         int64_t H, int topk, int64_t R, uint16_t* dy, float* dw,
                                         cudaStream_t stream, const DeviceInfo& dev) {
   const Launch l(M, kBackThreads, 0, stream);
-  return cudaLaunchKernelEx(&l.cfg, combine_backward_kernel, dout, y, dest, weights, (int)H, topk,
-                            R, dy, dw, dev.error_word);
+  const auto kernel = topk == 1   ? combine_backward_kernel<1, 8>
+                      : topk == 2 ? combine_backward_kernel<2, 4>
+                      : topk <= 4 ? combine_backward_kernel<4, 2>
+                                  : combine_backward_kernel<8, 1>;
+  return cudaLaunchKernelEx(&l.cfg, kernel, dout, y, dest, weights, (int)H, topk, R, dy, dw,
+                            dev.error_word);
 }
 
 }  // namespace gptq
