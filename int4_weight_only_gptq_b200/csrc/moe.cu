@@ -11,7 +11,7 @@
 // the combine with w = 1.  All of it is bound by memory traffic (or, for a few
 // tokens, by launch latency): rows move in 16-byte chunks, each input row is
 // read once, sums are FP32 in a fixed order (bitwise reproducible), and every
-// result is rounded once.  No kernel uses atomics on data it returns.
+// result is rounded once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -64,29 +64,38 @@ __device__ __forceinline__ int key_of(const Id* ids, int64_t p, int E) {
 // Every CTA holds all keys in shared memory and counts the places of its own
 // tokens' pairs directly from the definition of dest: O(pairs) work per pair,
 // which for up to kSortSmallPairs pairs takes less time than a second launch.
+// A key is expert * 4096 + p, so that dest is the number of smaller keys.
 // The last CTA writes the experts' offsets (a histogram and a scan).
-constexpr int kSortSmallPairs = 4096;
+constexpr int kSortSmallShift = 12;
+constexpr int kSortSmallPairs = 1 << kSortSmallShift;
 constexpr int kSmallThreads = 256;
 constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallAhead = 3;  // 16-byte chunks of a row per thread loaded ahead
 
 template <typename Id>
-__global__ void __launch_bounds__(kSmallThreads)
+__global__ void __launch_bounds__(kSmallThreads, 8)
     sort_small_kernel(const uint16_t* x, const Id* ids, int M, int H,
                       int topk, int E, uint16_t* x_sorted,
                       int32_t* offsets, int32_t* dest) {
-  extern __shared__ int keys[];
+  extern __shared__ __align__(16) int keys[];
   __shared__ int places[GPTQ_MOE_MAX_TOPK];
   __shared__ int counts[GPTQ_MOE_MAX_EXPERTS];
   wait_previous_grid();
   let_next_grid_start();
   const int P = M * topk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int p = threadIdx.x; p < P; p += kSmallThreads) keys[p] = key_of(ids, p, E);
+#pragma unroll 4
+  for (int p = threadIdx.x; p < P; p += kSmallThreads)
+    keys[p] = key_of(ids, p, E) << kSortSmallShift | p;
+  // to a multiple of four keys: the largest key there is
+  if ((int)threadIdx.x < 3) keys[P + threadIdx.x] = 0x7FFFFFFF;
   if ((int)blockIdx.x == gridDim.x - 1) {
     for (int e = threadIdx.x; e < E; e += kSmallThreads) counts[e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < P; p += kSmallThreads)
-      if (keys[p] < E) atomicAdd(&counts[keys[p]], 1);
+    for (int p = threadIdx.x; p < P; p += kSmallThreads) {
+      const int e = keys[p] >> kSortSmallShift;
+      if (e < E) atomicAdd(&counts[e], 1);
+    }
     __syncthreads();
     if (warp == 0) {
       int before = 0;
@@ -107,17 +116,24 @@ __global__ void __launch_bounds__(kSmallThreads)
   }
   __syncthreads();
   for (int m = blockIdx.x; m < M; m += gridDim.x - 1) {
+    // the row's first chunks are under way while the places are counted
+    const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)m * H);
+    const int chunks = H / 8;
+    uint4 v[kSmallAhead];
+#pragma unroll
+    for (int i = 0; i < kSmallAhead; ++i)
+      if ((int)threadIdx.x + i * kSmallThreads < chunks)
+        v[i] = ld_row_v4(src + threadIdx.x + i * kSmallThreads);
     for (int j = warp; j < topk; j += kSmallWarps) {
-      const int p = m * topk + j, e = keys[p];
-      int n = 0;
-      if (e < E) {
-        for (int q = lane; q < P; q += 32) {
-          const int k = keys[q];
-          n += (k < e || (k == e && q < p)) ? 1 : 0;
+      const int p = m * topk + j, key = keys[p];
+      int n = -1;
+      if (key >> kSortSmallShift < E) {
+        n = 0;
+        for (int q = lane; 4 * q < P; q += 32) {
+          const int4 k = reinterpret_cast<const int4*>(keys)[q];
+          n += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
         }
         n = __reduce_add_sync(0xffffffffu, n);
-      } else {
-        n = -1;
       }
       if (lane == 0) {
         places[j] = n;
@@ -125,12 +141,19 @@ __global__ void __launch_bounds__(kSmallThreads)
       }
     }
     __syncthreads();
-    const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)m * H);
-    for (int c = threadIdx.x; c < H / 8; c += kSmallThreads) {
-      const uint4 v = src[c];
+    for (int j = 0; j < topk; ++j) {
+      if (places[j] < 0) continue;
+      uint4* out = reinterpret_cast<uint4*>(x_sorted + (int64_t)places[j] * H);
+#pragma unroll
+      for (int i = 0; i < kSmallAhead; ++i)
+        if ((int)threadIdx.x + i * kSmallThreads < chunks)
+          out[threadIdx.x + i * kSmallThreads] = v[i];
+    }
+    for (int c = threadIdx.x + kSmallAhead * kSmallThreads; c < chunks; c += kSmallThreads) {
+      const uint4 more = ld_row_v4(src + c);
       for (int j = 0; j < topk; ++j)
         if (places[j] >= 0)
-          reinterpret_cast<uint4*>(x_sorted + (int64_t)places[j] * H)[c] = v;
+          reinterpret_cast<uint4*>(x_sorted + (int64_t)places[j] * H)[c] = more;
     }
     __syncthreads();
   }
@@ -139,15 +162,15 @@ __global__ void __launch_bounds__(kSmallThreads)
 // ---- sort, many pairs: places by one cluster, then the rows ------------------
 //
 // One cluster of eight CTAs; every warp owns a contiguous run of pairs and
-// walks it twice: once counting its pairs per expert (lanes with equal keys
-// found by a warp match; the first of them adds their number), once handing
-// out places from its running base per expert.  Between the walks the counts
+// walks it twice: once counting its pairs per expert, once handing out places
+// in order from its running base per expert.  Between the walks the counts
 // are turned into bases: over the warps of a CTA, over the CTAs (distributed
 // shared memory), over the experts.  The order of pairs is kept throughout, so
-// the sort is stable and needs no atomics and no scratch memory.
+// the sort is stable, and it needs no scratch memory.
 constexpr int kPlaceCtas = 8;
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWarps = kPlaceThreads / 32;
+constexpr int kPlaceKeys = 8;  // pairs per lane whose ids are loaded together
 
 constexpr size_t place_smem_bytes(int E) { return ((size_t)kPlaceWarps + 2) * E * sizeof(int); }
 
@@ -155,6 +178,27 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// Keys of pairs p, p + 32, ..., all loads in flight at once (one by one they
+// cost a memory latency each: 65,536 pairs took 22 us instead of 6).
+template <typename Id>
+__device__ __forceinline__ void load_keys(const Id* ids, int64_t p, int64_t end, int E,
+                                          int (&key)[kPlaceKeys]) {
+#pragma unroll
+  for (int i = 0; i < kPlaceKeys; ++i) key[i] = p + 32 * i < end ? key_of(ids, p + 32 * i, E) : E;
+}
+
+// The lanes whose key equals this lane's: one ballot per bit.  (A warp match
+// instruction takes a time that grows with the number of different keys: with
+// 128 experts it was 15 times slower.)
+__device__ __forceinline__ unsigned lanes_with_equal(int key, int key_bits) {
+  unsigned same = 0xffffffffu;
+  for (int b = 0; b < key_bits; ++b) {
+    const unsigned set = __ballot_sync(0xffffffffu, (key >> b) & 1);
+    same &= (key >> b) & 1 ? set : ~set;
+  }
+  return same;
 }
 
 template <typename Id>
@@ -178,20 +222,25 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
   int* mine = base + warp * E;
   for (int e = lane; e < E; e += 32) mine[e] = 0;
   __syncwarp();
-  for (int64_t p0 = begin; p0 < end; p0 += 32) {
-    const int64_t p = p0 + lane;
-    const int key = p < end ? key_of(ids, p, E) : E;
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    if (key < E && (same & ((1u << lane) - 1u)) == 0) mine[key] += __popc(same);
-    __syncwarp();
+  int key[kPlaceKeys];
+  for (int64_t p0 = begin; p0 < end; p0 += 32 * kPlaceKeys) {
+    load_keys(ids, p0 + lane, end, E, key);
+#pragma unroll
+    for (int i = 0; i < kPlaceKeys; ++i) {
+      if (p0 + 32 * i >= end) break;
+      if (key[i] < E) atomicAdd(&mine[key[i]], 1);
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kPlaceThreads) {
+    int c[kPlaceWarps];
+#pragma unroll
+    for (int v = 0; v < kPlaceWarps; ++v) c[v] = base[v * E + e];
     int sum = 0;
+#pragma unroll
     for (int v = 0; v < kPlaceWarps; ++v) {
-      const int c = base[v * E + e];
       base[v * E + e] = sum;
-      sum += c;
+      sum += c[v];
     }
     total[e] = sum;
   }
@@ -200,6 +249,7 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
   // CTAs before this one, then the scan over the experts
   int before = 0, all = 0;
   if ((int)threadIdx.x < E) {
+#pragma unroll
     for (int c = 0; c < kPlaceCtas; ++c) {
       const int n = ld_dsmem_s32(map_to_rank(smem_u32(&total[threadIdx.x]), (uint32_t)c));
       if (c < cta) before += n;
@@ -214,8 +264,8 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
   }
   if (lane == 31) warp_sums[warp] = scan;
   __syncthreads();
-  int prior = 0;
-  for (int v = 0; v < warp; ++v) prior += warp_sums[v];
+  int prior = lane < warp ? warp_sums[lane] : 0;  // 32 warps: one lane each
+  prior = __reduce_add_sync(0xffffffffu, prior);
   const int start = prior + scan - all;  // the expert's first row
   if ((int)threadIdx.x < E) {
     first[threadIdx.x] = start + before;
@@ -224,25 +274,38 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
       if ((int)threadIdx.x == E - 1) offsets[E] = start + all;
     }
   }
-  // no CTA leaves while another may still read its totals
-  cluster_sync_all();
+  // no CTA leaves while another may still read its totals: this one has read
+  // them, and waits for the others at its end
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  __syncthreads();  // first[] is complete
   for (int e = lane; e < E; e += 32) mine[e] += first[e];
   __syncwarp();
-  for (int64_t p0 = begin; p0 < end; p0 += 32) {
-    const int64_t p = p0 + lane;
-    const int key = p < end ? key_of(ids, p, E) : E;
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int lower = __popc(same & ((1u << lane) - 1u));
-    const int at = key < E ? mine[key] : 0;
-    __syncwarp();
-    if (key < E && lower == 0) mine[key] = at + __popc(same);
-    __syncwarp();
-    if (p < end) dest[p] = key < E ? at + lower : -1;
+  const int key_bits = 32 - __clz(E);  // keys are 0 .. E
+  const bool kept = end - begin <= 32 * kPlaceKeys;  // the first walk's keys are all still here
+  for (int64_t p0 = begin; p0 < end; p0 += 32 * kPlaceKeys) {
+    if (!kept) load_keys(ids, p0 + lane, end, E, key);
+#pragma unroll
+    for (int i = 0; i < kPlaceKeys; ++i) {
+      const int64_t p = p0 + 32 * i + lane;
+      if (p - lane >= end) break;
+      const unsigned same = lanes_with_equal(key[i], key_bits);
+      const int lower = __popc(same & ((1u << lane) - 1u));
+      const int at = key[i] < E ? mine[key[i]] : 0;
+      __syncwarp();
+      if (key[i] < E && lower == 0) mine[key[i]] = at + __popc(same);
+      __syncwarp();
+      if (p < end) dest[p] = key[i] < E ? at + lower : -1;
+    }
   }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Rows: a warp takes 1024 values (four 16-byte chunks per lane) of one token,
-// reads them once and writes them to each of the token's places.
+// reads them once and writes them to each of the token's places.  The grid
+// starts once every CTA of the places' launch has passed its own wait for
+// earlier work, so x is complete by then and its first loads run beside that
+// launch; only the places wait for it.
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kGatherChunks = 4;
@@ -252,16 +315,19 @@ __global__ void __launch_bounds__(kRowThreads)
                      int topk, int segments, uint16_t* x_sorted) {
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  wait_previous_grid();
-  let_next_grid_start();
   const int64_t m = unit / segments;
-  if (m >= M) return;
+  if (m >= M) {
+    wait_previous_grid();
+    return;
+  }
   const int c0 = (int)(unit - m * segments) * (32 * kGatherChunks) + lane, chunks = H / 8;
   const uint4* src = reinterpret_cast<const uint4*>(x + m * H);
   uint4 v[kGatherChunks];
 #pragma unroll
   for (int i = 0; i < kGatherChunks; ++i)
     if (c0 + 32 * i < chunks) v[i] = ld_row_v4(src + c0 + 32 * i);
+  wait_previous_grid();
+  let_next_grid_start();
   for (int j0 = 0; j0 < topk; j0 += 32) {
     const int mine = j0 + lane < topk ? dest[m * topk + j0 + lane] : -1;
     const int n = min(32, topk - j0);
@@ -457,7 +523,7 @@ cudaError_t launch_sort(const uint16_t* x, const Id* ids, int64_t M, int64_t H, 
   if (P <= kSortSmallPairs) {
     // one CTA per token up to eight per SM, and the one that writes offsets
     const int64_t ctas = std::min<int64_t>(M, 8 * (int64_t)dev.num_sms) + 1;
-    const Launch l(ctas, kSmallThreads, (size_t)P * sizeof(int), stream);
+    const Launch l(ctas, kSmallThreads, (size_t)(P + 3) * sizeof(int), stream);
     return cudaLaunchKernelEx(&l.cfg, sort_small_kernel<Id>, x, ids, (int)M, (int)H, topk, E,
                               x_sorted, offsets, dest);
   }
