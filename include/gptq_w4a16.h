@@ -335,6 +335,19 @@ GPTQ_API int gptq_w4a16_gemm_experts(const uint16_t* x_sorted, const int32_t* qw
                                      uint16_t* y_sorted, void* stream);
 
 /*
+ * As gptq_w4a16_gemm_experts, with the kernel forced: kernel_id is one of the
+ * GPTQ_KERNEL_* values, tile the most rows of an expert that share one pass
+ * over its weights (16, 32 or 64 with GPTQ_KERNEL_DECODE, 0 otherwise; else
+ * GPTQ_ERR_KERNEL).  Any choice gives a correct, deterministic result.  Meant
+ * for tests and benchmarks that compare the kernels on the same shape.
+ */
+GPTQ_API int gptq_w4a16_gemm_experts_kernel(const uint16_t* x_sorted, const int32_t* qweight,
+                                            const uint16_t* scales, const int32_t* offsets,
+                                            int64_t R, int64_t K, int64_t N, int64_t E,
+                                            int32_t group, uint16_t* y_sorted, void* stream,
+                                            int32_t kernel_id, int32_t tile);
+
+/*
  * The gradient of gptq_w4a16_gemm_experts with respect to its rows:
  *   dx_sorted[r] = dy_sorted[r] . dequant(qweight[e], scales[e])^T
  * dy_sorted [R, N] FP16 bits; dx_sorted [R, K] FP16 bits, written in the rows

@@ -38,8 +38,8 @@ EXPORTS = ("gptq_w4a16_gemm", "gptq_w4a16_gemm_kernel", "gptq_w4a16_gemm_decode_
            "gptq_w4a16_gemm_grouped", "gptq_w4a16_gemm_asym", "gptq_w4a16_gemm_gidx",
            "gptq_w4a16_gemm_lora", "gptq_w4a16_gemm_lora_noalloc",
            "gptq_moe_sort", "gptq_moe_combine", "gptq_moe_combine_backward",
-           "gptq_w4a16_gemm_experts", "gptq_w4a16_gemm_experts_dx",
-           "gptq_dequant",
+           "gptq_w4a16_gemm_experts", "gptq_w4a16_gemm_experts_kernel",
+           "gptq_w4a16_gemm_experts_dx", "gptq_dequant",
            "gptq_w4a16_select", "gptq_status_string", "gptq_device_error", "gptq_version")
 
 
@@ -85,6 +85,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                       _p, _p, _p]
             experts_args = [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _i32, _p, _p]
             lib.gptq_w4a16_gemm_experts.argtypes = experts_args
+            lib.gptq_w4a16_gemm_experts_kernel.argtypes = experts_args + [_i32, _i32]
             lib.gptq_w4a16_gemm_experts_dx.argtypes = experts_args
             lib.gptq_dequant.argtypes = [_p, _p, _i64, _i64, _i32, _p, _p]
             lib.gptq_w4a16_select.argtypes = [_i64, _i64, _i64, _i32,
@@ -98,8 +99,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                          "gptq_w4a16_gemm_asym", "gptq_w4a16_gemm_gidx", "gptq_w4a16_gemm_lora",
                          "gptq_w4a16_gemm_lora_noalloc",
                          "gptq_moe_sort", "gptq_moe_combine", "gptq_moe_combine_backward",
-                         "gptq_w4a16_gemm_experts", "gptq_w4a16_gemm_experts_dx",
-                         "gptq_dequant",
+                         "gptq_w4a16_gemm_experts", "gptq_w4a16_gemm_experts_kernel",
+                         "gptq_w4a16_gemm_experts_dx", "gptq_dequant",
                          "gptq_w4a16_select", "gptq_device_error"):
                 getattr(lib, name).restype = ctypes.c_int
             _lib = lib
@@ -513,6 +514,8 @@ def experts_shapes(rows, qweight, scales, offsets, group: int,
 
 
 def _experts(fn, rows, qweight, scales, offsets, group, out, stream, gradient, name):
+    """Checks and output of an experts' product, and its library call; `fn`
+    takes the entry's arguments without the kernel choice."""
     dev = qweight.device
     _require_moe(qweight, "qweight", torch.int32, dev)
     _require_moe(scales, "scales", torch.float16, dev)
@@ -531,14 +534,18 @@ def _experts(fn, rows, qweight, scales, offsets, group, out, stream, gradient, n
 
 def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
                  offsets: torch.Tensor, group: int, out: torch.Tensor | None = None,
-                 stream=None) -> torch.Tensor:
+                 stream=None, kernel: int = KERNEL_AUTO, tile: int = 0) -> torch.Tensor:
     """Every expert's linear on its own rows: y_sorted[r] = x_sorted[r] .
     dequant(qweight[e], scales[e]) for offsets[e] <= r < offsets[e + 1].
     x_sorted [R, K] FP16 and offsets [E + 1] int32 as moe_sort returns them,
     qweight [E, K/8, N] int32, scales [E, n_groups, N] FP16.  Rows that belong
-    to no expert keep what `out` holds."""
-    return _experts(load().gptq_w4a16_gemm_experts, x_sorted, qweight, scales, offsets, group,
-                    out, stream, False, "x_sorted")
+    to no expert keep what `out` holds.  kernel and tile force the kernel: tests
+    and benchmarks (KERNEL_DECODE takes a tile of 16, 32 or 64 rows)."""
+    lib = load()
+    fn = lib.gptq_w4a16_gemm_experts
+    if kernel != KERNEL_AUTO or tile != 0:
+        fn = lambda *args: lib.gptq_w4a16_gemm_experts_kernel(*args, kernel, tile)
+    return _experts(fn, x_sorted, qweight, scales, offsets, group, out, stream, False, "x_sorted")
 
 
 def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,

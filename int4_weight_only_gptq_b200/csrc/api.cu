@@ -240,13 +240,25 @@ int status_of(cudaError_t e) {
   return GPTQ_ERR_CUDA;
 }
 
+// The kernel of the experts' products, and its token tile, from the rows an
+// expert has on average.
+int select_experts_kernel(int64_t R, int64_t E, int32_t* tile) {
+  const int64_t mean = (R + E - 1) / E;
+  *tile = mean <= 6 ? 16 : mean <= 16 ? 32 : 64;
+  return mean <= 40 ? GPTQ_KERNEL_DECODE : GPTQ_KERNEL_PREFILL;
+}
+
 // The experts' products: in [R, K] -> out [R, N], or the gradient in [R, N]
 // -> out [R, K].
 int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* scales,
                  const int32_t* offsets, int64_t R, int64_t K, int64_t N, int64_t E,
-                 int32_t group, uint16_t* out, void* stream, bool gradient) {
+                 int32_t group, uint16_t* out, void* stream, bool gradient,
+                 int32_t kernel_id = GPTQ_KERNEL_AUTO, int32_t tile = 0) {
   int st = check_shape(R, K, N, group);
   if (st != GPTQ_OK) return st;
+  if (kernel_id < GPTQ_KERNEL_AUTO || kernel_id > GPTQ_KERNEL_PREFILL) return GPTQ_ERR_KERNEL;
+  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 16 && tile != 32 && tile != 64 : tile != 0)
+    return GPTQ_ERR_KERNEL;
   if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
   if (!qweight || !scales || !offsets) return GPTQ_ERR_NULL;
   if (R == 0) return GPTQ_OK;
@@ -264,9 +276,15 @@ int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* sca
   if (st != GPTQ_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int gs = group_shift_of(group);
-  return status_of(
-      gradient ? launch_experts_dx(in, qweight, scales, offsets, out, R, K, N, E, gs, s, *dev)
-               : launch_experts_pair(in, qweight, scales, offsets, out, R, K, N, E, gs, s, *dev));
+  if (gradient)
+    return status_of(
+        launch_experts_dx(in, qweight, scales, offsets, out, R, K, N, E, gs, s, *dev));
+  if (kernel_id == GPTQ_KERNEL_AUTO) kernel_id = select_experts_kernel(R, E, &tile);
+  return status_of(kernel_id == GPTQ_KERNEL_DECODE
+                       ? launch_experts_decode(in, qweight, scales, offsets, out, R, K, N, E, gs,
+                                               tile, s, *dev)
+                       : launch_experts_pair(in, qweight, scales, offsets, out, R, K, N, E, gs, s,
+                                             *dev));
 }
 
 }  // namespace
@@ -506,6 +524,15 @@ int gptq_w4a16_gemm_experts(const uint16_t* x_sorted, const int32_t* qweight,
                             void* stream) {
   return experts_impl(x_sorted, qweight, scales, offsets, R, K, N, E, group, y_sorted, stream,
                       false);
+}
+
+int gptq_w4a16_gemm_experts_kernel(const uint16_t* x_sorted, const int32_t* qweight,
+                                   const uint16_t* scales, const int32_t* offsets, int64_t R,
+                                   int64_t K, int64_t N, int64_t E, int32_t group,
+                                   uint16_t* y_sorted, void* stream, int32_t kernel_id,
+                                   int32_t tile) {
+  return experts_impl(x_sorted, qweight, scales, offsets, R, K, N, E, group, y_sorted, stream,
+                      false, kernel_id, tile);
 }
 
 int gptq_w4a16_gemm_experts_dx(const uint16_t* dy_sorted, const int32_t* qweight,

@@ -1,0 +1,557 @@
+// The experts' products for few rows per expert (decoding):
+//   Y[rows of e] = X[rows of e] . dequant(qweight[e], scales[e])
+// streaming each chosen expert's weights once.
+//
+// The transposed product of the decode kernel (a CTA owns 128 weight columns,
+// one TMEM lane each; the tokens are the MMA's N), with the token tiles cut
+// from the experts' rows (experts.cuh) and one persistent CTA per SM walking
+// the (token tile, column block) items, column block fastest:
+//
+// * Ring stages of 256 k: the qweight box [32 packed rows x 128 columns]
+//   (16 KB), its scale rows and X [rows x 256 k], all by TMA.  X comes in
+//   boxes of 8 or BT rows, whichever holds the tile; rows past the tile belong
+//   to other experts, each a column of the accumulator that is never stored.
+// * Three groups of four warps take the stages in turn, group g filling TMEM
+//   A slot g: a thread turns the 32 words of its column into 128 cells.  One
+//   wait for the stage, one for the slot and one arrival per 32 words: with
+//   sixteen words per warp between the barriers the waits were a third of all
+//   instructions, and issue slots bound this kernel.
+// * As in the decode kernel the words come out paired (k, k + 4), and the
+//   group permutes the tile's real X rows to the same order in place.
+// * One elected lane issues the MMAs, round-robin over NACC accumulators in
+//   one of two sets; four warps of their own read a finished item out and
+//   store it while the next one is multiplied.
+// * Few items (splits > 1): the CTAs of a cluster share one item, each taking
+//   a range of K, and add their partial sums in rank order through
+//   distributed shared memory.
+//
+// Weights are dequantised exactly as defined, fp16((q - 8) * s), FP32
+// accumulation, one rounding; the order of the sums is fixed, so results are
+// bitwise reproducible.  Every wait is bounded in time; on expiry the kernel
+// records GPTQ_ERR_TIMEOUT in the device error word, drains its own copies
+// and MMAs, frees TMEM and exits.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "common.cuh"
+#include "experts.cuh"
+#include "gptq_w4a16.h"
+#include "kernels.h"
+#include "tc05.cuh"
+#include "tmap.h"
+
+namespace gptq {
+
+namespace {
+
+constexpr int BW = 128;        // weight columns per item (MMA M)
+constexpr int BK = 256;        // k per stage and A slot fill (16 MMAs of k16)
+constexpr int PR = BK / 8;     // packed rows per stage
+constexpr int WPT = 8;         // words per TMEM store (32 columns)
+constexpr int GROUPS = 3;      // dequantisation groups, one per A slot
+constexpr int DQ_WARP0 = 2;    // warps 0, 1: TMA producer, MMA issuer
+constexpr int EPI_WARP0 = DQ_WARP0 + 4 * GROUPS;  // four read-out warps
+constexpr int THREADS = (EPI_WARP0 + 4) * 32;
+constexpr int QW_BYTES = PR * BW * 4;
+constexpr int QW_ROW_BYTES = BW * 4;
+constexpr int S_ROW_BYTES = BW * 2;
+constexpr int X_SMALL_ROWS = 8;  // the smaller X box
+constexpr int kMaxStages = 8;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t D_COL = 0;     // two accumulator sets of 64 columns
+constexpr uint32_t D_SET = 64;
+constexpr uint32_t A_COL = 128;   // A slots: [128, 512), 128 columns each
+constexpr uint32_t A_SLOT_COLS = BK / 2;
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr uint64_t kDrainLimitNs = 200000000ull;
+static_assert(A_COL + GROUPS * A_SLOT_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(EPI_WARP0 % 4 == 2 && DQ_WARP0 % 4 == 2, "quarters by warp % 4");
+
+struct Bars {
+  uint64_t full[kMaxStages];   // stage landed
+  uint64_t empty[kMaxStages];  // stage read by its group's warps and the MMAs
+  uint64_t afull[GROUPS];      // A slot written (and X permuted) by its group's warps
+  uint64_t aempty[GROUPS];     // MMAs reading the A slot done
+  uint64_t dfull[2];           // MMAs of an item done (set j % 2)
+  uint64_t dempty[2];          // accumulator set read out
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Shared memory: the ring, the barriers, the table of token tiles.
+constexpr int kSmemLimit = 227 * 1024 - 1024;
+
+struct Shape {
+  int scale_rows, stage_bytes, stages, smem_bytes;
+};
+
+template <int BT>
+Shape shape_of(int group_shift, int E) {
+  Shape d;
+  const int gs = group_shift < 30 ? group_shift : 30;
+  d.scale_rows = (BK >> gs) > 1 ? (BK >> gs) : 1;
+  d.stage_bytes = (BT * BK * 2 + QW_BYTES + d.scale_rows * S_ROW_BYTES + 1023) & ~1023;
+  const int rest = (int)sizeof(Bars) + ExpertTable<BT, 16>::bytes(E);
+  d.stages = std::min(kMaxStages, (kSmemLimit - rest) / d.stage_bytes);
+  d.smem_bytes = 1024 + d.stages * d.stage_bytes + rest;
+  return d;
+}
+
+struct XMaps {
+  CUtensorMap rows[2];  // boxes of X_SMALL_ROWS and BT rows
+};
+
+// One 16-byte chunk of an X row (eight consecutive k) rewritten in place from
+// natural order to the paired order of the unpacked weights.
+__device__ __forceinline__ void permute_x_chunk(uint8_t* p) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  uint4 o;
+  o.x = prmt(v.x, v.z, 0x5410);
+  o.y = prmt(v.x, v.z, 0x7632);
+  o.z = prmt(v.y, v.w, 0x5410);
+  o.w = prmt(v.y, v.w, 0x7632);
+  *reinterpret_cast<uint4*>(p) = o;
+}
+
+// WPS: consecutive words of a thread that share one scale (2: group 16, 4:
+// group 32, 8: larger ones).  x3d: X as one 3-D box per stage (K a multiple of
+// 64), else one 2-D box per 64 k.  gridDim.y: CTAs (a cluster) that share an
+// item along K.
+template <int WPS, int BT>
+__global__ void __launch_bounds__(THREADS, 1)
+    experts_decode_kernel(const __grid_constant__ XMaps x_maps,
+                          const __grid_constant__ CUtensorMap qw_map,
+                          const __grid_constant__ CUtensorMap s_map, const int32_t* offsets,
+                          uint16_t* y, int R, int K, int N, int E, int group_shift, int stages,
+                          int stage_bytes, int scale_rows, int x3d, int* err) {
+  // independent accumulators: MMAs into one accumulator run one after another
+  constexpr int NACC = D_SET / BT < 4 ? D_SET / BT : 4;
+  using Table = ExpertTable<BT, 16>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* bar = reinterpret_cast<Bars*>(ring + stages * stage_bytes);
+  volatile int* abort_flag = &bar->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gs = min(group_shift, 30);
+  const int splits = gridDim.y;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&bar->full[s], 1);
+      mbar_init(&bar->empty[s], 4 + 1);  // the group's warps + the MMA commit
+    }
+    for (int a = 0; a < GROUPS; ++a) {
+      mbar_init(&bar->afull[a], 4);
+      mbar_init(&bar->aempty[a], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->dfull[i], 1);
+      mbar_init(&bar->dempty[i], 4);
+    }
+    bar->abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&x_maps.rows[0]);
+    prefetch_tensormap(&x_maps.rows[1]);
+    prefetch_tensormap(&qw_map);
+    prefetch_tensormap(&s_map);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bar->tmem_base, TMEM_COLS);
+    tmem_relinquish();
+  }
+  // the offsets and X may come from the previous kernel of the stream
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Table table;
+  table.place(bar + 1, E);
+  tc_fence_before();
+  table.build(offsets, R, THREADS, err);  // ends with a barrier of the CTA
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+
+  const int nblk = (N + BW - 1) / BW;
+  const int items = table.tiles() * nblk;
+  const int first = blockIdx.x, step = gridDim.x;
+  const int n_items = first < items ? (items - first + step - 1) / step : 0;
+  const int NS = (K + BK - 1) / BK;
+  const int st0 = (int)((int64_t)blockIdx.y * NS / splits);  // this CTA's stages of an item
+  const int n_st = (int)((int64_t)(blockIdx.y + 1) * NS / splits) - st0;
+
+  if (warp == 0) {
+    // ---------------- TMA producer (one lane) ----------------
+    if (lane == 0) {
+      int issued = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int j = 0; j < n_items && ok; ++j) {
+        const int item = first + j * step;
+        const ExpertTile tt = table.find(item / nblk);
+        const int n0 = (item % nblk) * BW;
+        const int big = tt.rows > X_SMALL_ROWS;
+        const CUtensorMap* xm = &x_maps.rows[big];
+        const int atom_bytes = (big ? BT : X_SMALL_ROWS) * 128;
+        for (int t = 0; t < n_st; ++t) {
+          if (!mbar_wait_bounded(&bar->empty[s], ph ^ 1u, abort_flag, kWaitLimitNs)) {
+            record_timeout(err, bar);
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + s * stage_bytes;
+          const int k0 = (st0 + t) * BK;
+          // 64-k atoms of X that hold k below K (a 3-D box always fills four)
+          const int atoms = x3d ? 4 : min(4, (K - k0 + 63) / 64);
+          mbar_arrive_expect_tx(&bar->full[s],
+                                QW_BYTES + scale_rows * S_ROW_BYTES + atoms * atom_bytes);
+          tma_load_3d(st + BT * BK * 2, &qw_map, n0, k0 >> 3, tt.e, &bar->full[s]);
+          tma_load_3d(st + BT * BK * 2 + QW_BYTES, &s_map, n0, k0 >> gs, tt.e, &bar->full[s]);
+          if (x3d) {
+            tma_load_3d(st, xm, 0, tt.row0, k0 >> 6, &bar->full[s]);
+          } else {
+            for (int a = 0; a < atoms; ++a)
+              tma_load_2d(st + a * atom_bytes, xm, k0 + 64 * a, tt.row0, &bar->full[s]);
+          }
+          ++issued;
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (*abort_flag) {
+        // drain: wait (bounded) for the last load issued into each slot
+        int never = 0;
+        for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
+          mbar_wait_bounded(&bar->full[i % stages], (uint32_t)(i / stages) & 1u, &never,
+                            kDrainLimitNs);
+      }
+      // all copies are issued: the next kernel in the stream may start its
+      // prologue (it waits for this grid before touching its inputs)
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (converged; one elected lane issues) ----------------
+    bool ok = true;
+    int s = 0, a = 0, j = 0;
+    uint32_t ph = 0, aph = 0;
+    for (; j < n_items && ok; ++j) {
+      const ExpertTile tt = table.find((first + j * step) / nblk);
+      const uint32_t idesc = idesc_f16_f32(BW, tt.n);
+      const uint32_t atom_bytes = (tt.rows > X_SMALL_ROWS ? BT : X_SMALL_ROWS) * 128;
+      const uint32_t d_base = tmem + D_COL + (uint32_t)(j & 1) * D_SET;
+      if (j >= 2) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&bar->dempty[j & 1], (uint32_t)((j - 2) >> 1) & 1u,
+                                          abort_flag, kWaitLimitNs));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      for (int t = 0; t < n_st; ++t) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&bar->full[s], ph, abort_flag, kWaitLimitNs) &&
+                            mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
+        const uint32_t a_base = tmem + A_COL + a * A_SLOT_COLS;
+        const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            if (kk < nk)
+              mma_f16_ts(d_base + (kk % NACC) * BT, a_base + 8 * kk,
+                         x_desc + (uint64_t)(((kk >> 2) * atom_bytes + (kk & 3) * 32) >> 4),
+                         idesc, t > 0 || kk >= NACC ? 1u : 0u);
+          mma_commit(&bar->aempty[a]);
+          mma_commit(&bar->empty[s]);
+          if (t == n_st - 1) mma_commit(&bar->dfull[j & 1]);
+        }
+        __syncwarp();
+        if (++a == GROUPS) {
+          a = 0;
+          aph ^= 1u;
+        }
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      if (lane == 0) record_timeout(err, bar);
+      // wait (bounded) for the MMAs already issued before TMEM is freed
+      if (elect_one()) mma_commit(&bar->aempty[a]);
+      __syncwarp();
+      int never = 0;
+      mbar_wait_bounded(&bar->aempty[a], aph, &never, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp < EPI_WARP0) {
+    // ---------------- dequantisation ----------------
+    const int grp = (warp - DQ_WARP0) >> 2;  // stages t = grp mod GROUPS, A slot grp
+    const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
+    const int col = 32 * quarter + lane;
+    const int gid = ((warp - DQ_WARP0) & 3) * 32 + lane;
+    const uint32_t a_slot = tmem + ((uint32_t)(32 * quarter) << 16) + A_COL + grp * A_SLOT_COLS;
+    const int total = n_items * n_st;
+    int s = grp % stages;
+    uint32_t ph = (uint32_t)(grp / stages) & 1u, aph = 0;
+    int j = -1, t = grp - GROUPS;  // item, and stage in it
+    int rows = 0, atom_bytes = 0;
+    bool ok = true;
+    for (int f = grp; f < total; f += GROUPS) {
+      t += GROUPS;
+      while (j < 0 || t >= n_st) {
+        if (j >= 0) t -= n_st;
+        ++j;
+        const ExpertTile tt = table.find((first + j * step) / nblk);
+        rows = tt.rows;
+        atom_bytes = (tt.rows > X_SMALL_ROWS ? BT : X_SMALL_ROWS) * 128;
+      }
+      const int k_left = K - (st0 + t) * BK;  // k below K from the stage's first on
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->full[s], ph, abort_flag, kWaitLimitNs));
+      if (!ok) break;
+      uint8_t* st = ring + s * stage_bytes;
+      // 32 chunks per row and stage: chunk c of 64-k atom c / 8 (every chunk of
+      // a row is permuted, so the swizzle does not matter)
+      for (int i = gid; i < 32 * rows; i += 128)
+        permute_x_chunk(st + ((i & 31) >> 3) * atom_bytes + (i >> 5) * 128 + (i & 7) * 16);
+      const uint8_t* qw = st + BT * BK * 2 + col * 4;
+      const uint8_t* sc = st + BT * BK * 2 + QW_BYTES + col * 2;
+#pragma unroll
+      for (int c = 0; c < PR / WPT; ++c) {
+        uint32_t cells[4 * WPT];
+        if (64 * c < k_left) {
+#pragma unroll
+          for (int g = 0; g < WPT / WPS; ++g) {
+            const int r0 = WPT * c + WPS * g;
+            const int srow = (8 * r0) >> gs;
+            const uint32_t s2 =
+                half2_broadcast(*reinterpret_cast<const uint16_t*>(sc + srow * S_ROW_BYTES));
+            uint32_t w[WPS];
+#pragma unroll
+            for (int i = 0; i < WPS; ++i)
+              w[i] = *reinterpret_cast<const uint32_t*>(qw + (r0 + i) * QW_ROW_BYTES);
+            if (WPS >= 4 && scale_fits_subnormal_form(s2)) {
+              uint32_t b2, c2;
+              subnormal_form_constants(s2, b2, c2);
+#pragma unroll
+              for (int i = 0; i < WPS; ++i)
+                dequant_word_paired_small_scale(w[i], s2, b2, c2, cells + 4 * (WPS * g + i));
+            } else {
+#pragma unroll
+              for (int i = 0; i < WPS; ++i)
+                dequant_word_paired(w[i], s2, cells + 4 * (WPS * g + i));
+            }
+          }
+        }
+        if (c == PR / WPT - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->empty[s]);  // qweight and scales of the stage read
+        }
+        if (c == 0) {
+          // the A slot is free once the MMAs of its previous use have completed
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->aempty[grp], aph ^ 1u, abort_flag,
+                                                         kWaitLimitNs));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (64 * c < k_left) tmem_st_32x32b_x32(a_slot + 4 * WPT * c, cells);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      fence_proxy_async_smem();  // the permuted X rows, for the MMAs
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->afull[grp]);
+      aph ^= 1u;
+      s += GROUPS;
+      if (s >= stages) {
+        s -= stages;
+        ph ^= 1u;
+      }
+    }
+    if (!ok && lane == 0) record_timeout(err, bar);
+    __syncwarp();
+  } else {
+    // ---------------- read-out ----------------
+    const int quarter = warp & 3;
+    const int col = 32 * quarter + lane;
+    const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
+    float* part = reinterpret_cast<float*>(ring);  // [token][column], splits > 1
+    // accumulators that hold something (fewer when K ends within the first)
+    const int nacc = min(NACC, (K - st0 * BK) / 16);
+    for (int j = 0; j < n_items; ++j) {
+      const int item = first + j * step;
+      const ExpertTile tt = table.find(item / nblk);
+      const int n = (item % nblk) * BW + col;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_bounded<true>(&bar->dfull[j & 1], (uint32_t)(j >> 1) & 1u,
+                                              abort_flag, kWaitLimitNs))) {
+        if (lane == 0) record_timeout(err, bar);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_set = tmem + lane_addr + D_COL + (uint32_t)(j & 1) * D_SET;
+      uint16_t* out = y + (int64_t)tt.row0 * N + n;
+#pragma unroll 1
+      for (int tb = 0; tb < tt.n / 16; ++tb) {
+        // the block's accumulators requested at once, summed in a fixed order
+        uint32_t v[NACC][16];
+#pragma unroll
+        for (int c = 0; c < NACC; ++c) tmem_ld_32x32b_x16(d_set + c * BT + 16 * tb, v[c]);
+        tmem_wait_ld();
+        if (16 * (tb + 1) == tt.n) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->dempty[j & 1]);  // the set may be overwritten
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          float acc = __uint_as_float(v[0][q]);
+#pragma unroll
+          for (int c = 1; c < NACC; ++c)
+            if (c < nacc) acc += __uint_as_float(v[c][q]);
+          const int tok = 16 * tb + q;
+          if (splits > 1)
+            part[tok * BW + col] = acc;
+          else if (tok < tt.rows && n < N)
+            out[(int64_t)tok * N] = __half_as_ushort(__float2half_rn(acc));
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  // Each CTA-wide barrier has a single call site reached by every thread.
+  tc_fence_before();
+  __syncthreads();
+  if (splits > 1) {
+    // one item per cluster: its CTAs add their ranges of K in rank order
+    cluster_sync_all();
+    if (first < items) {
+      const ExpertTile tt = table.find(first / nblk);
+      const int n0 = (first % nblk) * BW, rank = (int)cluster_ctarank();
+      const int count = tt.rows * BW;
+      const uint32_t base = smem_u32(ring);
+      for (int i = rank * count / splits + (int)threadIdx.x; i < (rank + 1) * count / splits;
+           i += THREADS) {
+        const int tok = i / BW, c = i - tok * BW;
+        if (n0 + c >= N) continue;
+        float sum = 0.f;
+        for (int r = 0; r < splits; ++r) sum += ld_dsmem_f32(map_to_rank(base + 4u * i, r));
+        y[(int64_t)(tt.row0 + tok) * N + n0 + c] = __half_as_ushort(__float2half_rn(sum));
+      }
+    }
+    cluster_sync_all();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <int WPS, int BT>
+cudaError_t launch_t(const XMaps& x_maps, const CUtensorMap& qw_map, const CUtensorMap& s_map,
+                     const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
+                     int64_t E, int group_shift, const Shape& d, int x3d, int64_t items,
+                     int splits, cudaStream_t stream, const DeviceInfo& dev) {
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  const int di = dev.device & 63;
+  std::call_once(once[di], [&] {
+    attr_err[di] = cudaFuncSetAttribute(experts_decode_kernel<WPS, BT>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        1024 + kSmemLimit);
+  });
+  if (attr_err[di] != cudaSuccess) return attr_err[di];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, std::max(1, dev.num_sms / splits)),
+                     (unsigned)splits, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)d.smem_bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = (unsigned)splits;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, experts_decode_kernel<WPS, BT>, x_maps, qw_map, s_map, offsets,
+                            y, (int)R, (int)K, (int)N, (int)E, group_shift, d.stages,
+                            d.stage_bytes, d.scale_rows, x3d, dev.error_word);
+}
+
+// CTAs that share an item along K: as many as the SMs hold when every item is
+// there, each with two stages at least (a shorter range does not pay for the
+// reduction).
+int pick_splits(int64_t items, int64_t K, const DeviceInfo& dev) {
+  const int64_t stages = (K + BK - 1) / BK;
+  int64_t s = std::min<int64_t>(8, dev.num_sms / items);
+  s = std::min(s, stages / 2);
+  return s < 1 ? 1 : (int)s;
+}
+
+template <int BT>
+cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+                      const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
+                      int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
+  const Shape d = shape_of<BT>(group_shift, (int)E);
+  if (d.stages < GROUPS) return cudaErrorInvalidValue;
+  const int64_t n_groups = (group_shift == 62 || (int64_t(1) << group_shift) >= K)
+                               ? 1 : (K + (int64_t(1) << group_shift) - 1) >> group_shift;
+  XMaps x_maps;
+  CUtensorMap qw_map, s_map;
+  const int x3d = K % 64 == 0;
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t rows = i ? BT : X_SMALL_ROWS;
+    const uint64_t dims[3] = {64, (uint64_t)R, (uint64_t)(K / 64)};
+    const uint64_t strides[2] = {(uint64_t)K * 2, 128};
+    const uint32_t box[3] = {64, rows, BK / 64};
+    if (!(x3d ? encode_map_3d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_128B)
+              : encode_map_2d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)K,
+                              (uint64_t)R, (uint64_t)K * 2, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B)))
+      return cudaErrorInvalidValue;
+  }
+  const uint64_t qdims[3] = {(uint64_t)N, (uint64_t)(K / 8), (uint64_t)E};
+  const uint64_t qstrides[2] = {(uint64_t)N * 4, (uint64_t)(K / 8) * N * 4};
+  const uint32_t qbox[3] = {BW, PR, 1};
+  const uint64_t sdims[3] = {(uint64_t)N, (uint64_t)n_groups, (uint64_t)E};
+  const uint64_t sstrides[2] = {(uint64_t)N * 2, (uint64_t)n_groups * N * 2};
+  const uint32_t sbox[3] = {BW, (uint32_t)d.scale_rows, 1};
+  if (!encode_map_3d(&qw_map, qweight, CU_TENSOR_MAP_DATA_TYPE_INT32, qdims, qstrides, qbox,
+                     CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_map_3d(&s_map, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, sdims, sstrides, sbox,
+                     CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  // the most items there can be: a tile per row, or one per expert and one
+  // more for every BT / 2 rows beyond that (tiles are at least half full)
+  const int64_t tiles = std::min<int64_t>(R, E + R / (BT / 2));
+  const int64_t items = tiles * ((N + BW - 1) / BW);
+  const int splits = pick_splits(items, K, dev);
+  const auto launch = group_shift == 4   ? launch_t<2, BT>
+                      : group_shift == 5 ? launch_t<4, BT>
+                                         : launch_t<WPT, BT>;
+  return launch(x_maps, qw_map, s_map, offsets, y, R, K, N, E, group_shift, d, x3d, items, splits,
+                stream, dev);
+}
+
+}  // namespace
+
+cudaError_t launch_experts_decode(const uint16_t* x, const int32_t* qweight,
+                                  const uint16_t* scales, const int32_t* offsets, uint16_t* y,
+                                  int64_t R, int64_t K, int64_t N, int64_t E, int group_shift,
+                                  int tile, cudaStream_t stream, const DeviceInfo& dev) {
+  const auto launch = tile <= 16 ? launch_bt<16> : tile <= 32 ? launch_bt<32> : launch_bt<64>;
+  return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
+}
+
+}  // namespace gptq

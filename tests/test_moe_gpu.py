@@ -239,7 +239,8 @@ def test_product(case, gradient):
     ref, size = P.product(rows, P.expert_weights(q, s, G), offsets, gradient)
     live = int(offsets[-1])
     out = Guarded(rows.shape[0], K if gradient else N, seed=3)
-    run = B.gemm_experts_dx if gradient else B.gemm_experts
+    kw = {} if gradient else dict(kernel=B.KERNEL_PREFILL)
+    run = lambda *a, **k: (B.gemm_experts_dx if gradient else B.gemm_experts)(*a, **k, **kw)
     run(cu(rows), cu(q), cu(s), cu(offsets), G, out=out.t)
     got = out.after()
     assert np.array_equal(bits(got[live:]), bits(out.before()[live:]))
@@ -247,6 +248,36 @@ def test_product(case, gradient):
            P.product_tol(ref[:live], size[:live], N if gradient else K),
            f"{'dx' if gradient else 'y'} E={len(counts)} K={K} N={N} G={G}")
     again = run(cu(rows), cu(q), cu(s), cu(offsets), G).cpu().numpy()
+    assert np.array_equal(bits(again[:live]), bits(got[:live]))
+
+
+DECODE = [  # more for the kernel of few rows: (rows per expert, K, N, G, rows behind)
+    ([1], 4096, 72, 128, 0),              # a cluster of eight shares the item
+    ([1, 0, 2], 1536, 264, 64, 1),        # ... of three stages' worth
+    ([9, 20, 7], 784, 136, 16, 2),        # K no multiple of 64: boxes of 64 k
+    ([64, 65, 31, 33, 17, 15, 128], 320, 1032, 32, 0),
+    ([3] * 40, 512, 640, -1, 4),          # more items than SMs
+    ([2] * 37, 64, 1024, 128, 0),         # one stage per item
+    ([70, 1, 30] * 20, 208, 520, 32, 3),
+]
+
+
+@pytest.mark.parametrize("case", PRODUCT + DECODE,
+                         ids=lambda c: f"E{len(c[0])}-K{c[1]}-N{c[2]}-G{c[3]}")
+@pytest.mark.parametrize("tile", [16, 32, 64])
+def test_product_of_few_rows(case, tile):
+    counts, K, N, G, tail = case
+    rows, q, s, offsets = product_inputs(case, False)
+    ref, size = P.product(rows, P.expert_weights(q, s, G), offsets)
+    live = int(offsets[-1])
+    out = Guarded(rows.shape[0], N, seed=4)
+    args = (cu(rows), cu(q), cu(s), cu(offsets), G)
+    B.gemm_experts(*args, out=out.t, kernel=B.KERNEL_DECODE, tile=tile)
+    got = out.after()
+    assert np.array_equal(bits(got[live:]), bits(out.before()[live:]))
+    within(got[:live], ref[:live], P.product_tol(ref[:live], size[:live], K),
+           f"tile {tile} E={len(counts)} K={K} N={N} G={G}")
+    again = B.gemm_experts(*args, kernel=B.KERNEL_DECODE, tile=tile).cpu().numpy()
     assert np.array_equal(bits(again[:live]), bits(got[:live]))
 
 
@@ -269,13 +300,15 @@ def test_one_hot_rows_reproduce_weights(counts, G):
     R = int(offsets[-1])
     expert = np.searchsorted(offsets, np.arange(R), side="right") - 1
     keep = expert != 1
-    for gradient in (False, True):
+    decode = [dict(kernel=B.KERNEL_DECODE, tile=t) for t in (16, 32, 64)]
+    for kw in [{}, dict(kernel=B.KERNEL_PREFILL), *decode, None]:
+        gradient = kw is None
         width = N if gradient else K
         hot = rng.integers(0, width, R)
         rows = np.zeros((R, width), np.float16)
         rows[np.arange(R), hot] = 1.0
-        run = B.gemm_experts_dx if gradient else B.gemm_experts
-        got = run(cu(rows), *args).cpu().numpy()[keep]
+        got = (B.gemm_experts_dx(cu(rows), *args) if gradient
+               else B.gemm_experts(cu(rows), *args, **kw)).cpu().numpy()[keep]
         want = np.stack([w[e, :, h] if gradient else w[e, h] for e, h in zip(expert, hot)])[keep]
         # a sum with zeros has no negative zero
         assert np.array_equal(bits(got + np.float16(0)), bits(want + np.float16(0)))
@@ -299,6 +332,16 @@ def test_a_row_with_nan_touches_no_other(counts, gradient):
     others[[1, offsets[1]]] = False
     assert np.array_equal(bits(a[others]), bits(b[others]))
     assert np.isnan(b[1]).all() and not np.isfinite(b[offsets[1]]).any()
+
+
+@pytest.mark.parametrize("kernel,tile", [(3, 0), (-1, 0), (1, 0), (1, 48), (2, 16), (0, 16)])
+def test_bad_kernel_choices_are_refused(kernel, tile):
+    rng = np.random.default_rng(1)
+    q, s = P.make_weights(rng, 2, 64, 32, 32)
+    with pytest.raises(B.GptqError) as e:
+        B.gemm_experts(cu(P.make_rows(rng, 4, 64)), cu(q), cu(s), cu(P.offsets_of([2, 2])), 32,
+                       kernel=kernel, tile=tile)
+    assert e.value.status == 9
 
 
 @pytest.mark.parametrize("offsets", [[0, 5, 3, 8], [0, 4, 9, 11], [-3, 2, 5, 8], [0, 8, 8, 4]])

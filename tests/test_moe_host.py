@@ -99,6 +99,12 @@ def test_experts_argument_checks(lib, name, kw, status):
     assert experts(lib, name, **kw) == status
 
 
+@pytest.mark.parametrize("kernel,tile", [(3, 0), (-1, 0), (1, 0), (1, 48), (2, 16), (0, 16)])
+def test_experts_kernel_choice_checks(lib, kernel, tile):
+    args = [v(a) for a in A[:4]] + [8, 64, 64, 8, 32, v(A[4]), None]
+    assert lib.gptq_w4a16_gemm_experts_kernel(*args, kernel, tile) == 9
+
+
 def test_empty_calls_are_no_ops(lib):
     assert combine(lib, M=0, y=0, dest=0, out=0) == 0
     assert backward(lib, M=0, g=0, y=0, dest=0, w=0, dy=0, dw=0) == 0
