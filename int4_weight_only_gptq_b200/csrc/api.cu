@@ -244,7 +244,7 @@ int status_of(cudaError_t e) {
 // expert has on average.
 int select_experts_kernel(int64_t R, int64_t E, int32_t* tile) {
   const int64_t mean = (R + E - 1) / E;
-  *tile = mean <= 6 ? 16 : mean <= 16 ? 32 : 64;
+  *tile = mean <= 2 ? 8 : mean <= 6 ? 16 : mean <= 16 ? 32 : 64;
   return mean <= 40 ? GPTQ_KERNEL_DECODE : GPTQ_KERNEL_PREFILL;
 }
 
@@ -257,7 +257,7 @@ int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* sca
   int st = check_shape(R, K, N, group);
   if (st != GPTQ_OK) return st;
   if (kernel_id < GPTQ_KERNEL_AUTO || kernel_id > GPTQ_KERNEL_PREFILL) return GPTQ_ERR_KERNEL;
-  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 16 && tile != 32 && tile != 64 : tile != 0)
+  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 8 && tile != 16 && tile != 32 && tile != 64 : tile != 0)
     return GPTQ_ERR_KERNEL;
   if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
   if (!qweight || !scales || !offsets) return GPTQ_ERR_NULL;

@@ -8,19 +8,23 @@
 // the (token tile, column block) items, column block fastest:
 //
 // * Ring stages of 256 k: the qweight box [32 packed rows x 128 columns]
-//   (16 KB), its scale rows and X [rows x 256 k], all by TMA.  X comes in
-//   boxes of 8 or BT rows, whichever holds the tile; rows past the tile belong
-//   to other experts, each a column of the accumulator that is never stored.
-// * Three groups of four warps take the stages in turn, group g filling TMEM
-//   A slot g: a thread turns the 32 words of its column into 128 cells.  One
-//   wait for the stage, one for the slot and one arrival per 32 words: with
+//   (16 KB), its scale rows and X [ROWS x 256 k], all by TMA.  Rows of X past
+//   the tile belong to other experts, each a column of the accumulator that is
+//   never stored.
+// * Four groups of four warps take the stages in turn; stage f goes to TMEM A
+//   slot f mod 3: a thread turns the 32 words of its column into 128 cells.
+//   One wait for the stage, one for the slot and one arrival per 32 words: with
 //   sixteen words per warp between the barriers the waits were a third of all
-//   instructions, and issue slots bound this kernel.
+//   instructions.
 // * As in the decode kernel the words come out paired (k, k + 4), and the
 //   group permutes the tile's real X rows to the same order in place.
-// * One elected lane issues the MMAs, round-robin over NACC accumulators in
-//   one of two sets; four warps of their own read a finished item out and
-//   store it while the next one is multiplied.
+// * One elected lane issues the MMAs into one of two accumulators; four warps
+//   of their own read a finished item out and store it while the next one is
+//   multiplied.  (An MMA of 16 tokens takes 15 cycles, into one accumulator or
+//   into four in turn.)  Everything that the descriptors are made of stays
+//   warp-uniform: a branch on the tile's rows inside the issue took the stage's
+//   sixteen MMAs from 310 to over 600 cycles, and its sequence bounds the
+//   kernel as much as the dequantisation does.
 // * Few items (splits > 1): the CTAs of a cluster share one item, each taking
 //   a range of K, and add their partial sums in rank order through
 //   distributed shared memory.
@@ -51,32 +55,42 @@ constexpr int BW = 128;        // weight columns per item (MMA M)
 constexpr int BK = 256;        // k per stage and A slot fill (16 MMAs of k16)
 constexpr int PR = BK / 8;     // packed rows per stage
 constexpr int WPT = 8;         // words per TMEM store (32 columns)
-constexpr int GROUPS = 3;      // dequantisation groups, one per A slot
+constexpr int GROUPS = 4;      // dequantisation groups: stage f goes to group f mod 4
+constexpr int SLOTS = 3;       // A slots: stage f goes to slot f mod 3
 constexpr int DQ_WARP0 = 2;    // warps 0, 1: TMA producer, MMA issuer
 constexpr int EPI_WARP0 = DQ_WARP0 + 4 * GROUPS;  // four read-out warps
 constexpr int THREADS = (EPI_WARP0 + 4) * 32;
 constexpr int QW_BYTES = PR * BW * 4;
 constexpr int QW_ROW_BYTES = BW * 4;
 constexpr int S_ROW_BYTES = BW * 2;
-constexpr int X_SMALL_ROWS = 8;  // the smaller X box
 constexpr int kMaxStages = 8;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t D_COL = 0;     // two accumulator sets of 64 columns
-constexpr uint32_t D_SET = 64;
+constexpr uint32_t D_COL = 0;     // two accumulators of up to 64 columns
+constexpr uint32_t D_NEXT = 64;
 constexpr uint32_t A_COL = 128;   // A slots: [128, 512), 128 columns each
 constexpr uint32_t A_SLOT_COLS = BK / 2;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
-static_assert(A_COL + GROUPS * A_SLOT_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(A_COL + SLOTS * A_SLOT_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(GROUPS < 2 * SLOTS, "see Bars::aempty");
 static_assert(EPI_WARP0 % 4 == 2 && DQ_WARP0 % 4 == 2, "quarters by warp % 4");
 
 struct Bars {
-  uint64_t full[kMaxStages];   // stage landed
+  // Use v of ring stage s landed: barrier s + stages * (v & 1).  A group can
+  // come to wait for a load that is not issued yet, with the stage's load
+  // before it (another group's, when the ring is no multiple of the groups)
+  // still under way: the two parities of one barrier could not tell them apart.
+  uint64_t full[2 * kMaxStages];
   uint64_t empty[kMaxStages];  // stage read by its group's warps and the MMAs
-  uint64_t afull[GROUPS];      // A slot written (and X permuted) by its group's warps
-  uint64_t aempty[GROUPS];     // MMAs reading the A slot done
-  uint64_t dfull[2];           // MMAs of an item done (set j % 2)
-  uint64_t dempty[2];          // accumulator set read out
+  uint64_t afull[SLOTS];       // A slot written (and X permuted) by a group's warps
+  // MMAs reading use u of slot a done: barrier a + SLOTS * (u & 1).  A group
+  // can come to wait for use u - 1 = stage f - 3 while the MMAs of stage f - 6
+  // (use u - 2) still run, which one barrier per slot and its parity could not
+  // tell from use u - 1 having finished; those of stage f - 9 are done, since
+  // the group's own stage f - 4 waited for stage f - 7.
+  uint64_t aempty[2 * SLOTS];
+  uint64_t dfull[2];           // MMAs of item j done (accumulator j % 2)
+  uint64_t dempty[2];          // accumulator read out
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -88,21 +102,17 @@ struct Shape {
   int scale_rows, stage_bytes, stages, smem_bytes;
 };
 
-template <int BT>
+template <int ROWS>
 Shape shape_of(int group_shift, int E) {
   Shape d;
   const int gs = group_shift < 30 ? group_shift : 30;
   d.scale_rows = (BK >> gs) > 1 ? (BK >> gs) : 1;
-  d.stage_bytes = (BT * BK * 2 + QW_BYTES + d.scale_rows * S_ROW_BYTES + 1023) & ~1023;
-  const int rest = (int)sizeof(Bars) + ExpertTable<BT, 16>::bytes(E);
+  d.stage_bytes = (ROWS * BK * 2 + QW_BYTES + d.scale_rows * S_ROW_BYTES + 1023) & ~1023;
+  const int rest = (int)sizeof(Bars) + ExpertTable<ROWS, ROWS>::bytes(E);
   d.stages = std::min(kMaxStages, (kSmemLimit - rest) / d.stage_bytes);
   d.smem_bytes = 1024 + d.stages * d.stage_bytes + rest;
   return d;
 }
-
-struct XMaps {
-  CUtensorMap rows[2];  // boxes of X_SMALL_ROWS and BT rows
-};
 
 // One 16-byte chunk of an X row (eight consecutive k) rewritten in place from
 // natural order to the paired order of the unpacked weights.
@@ -119,17 +129,18 @@ __device__ __forceinline__ void permute_x_chunk(uint8_t* p) {
 // WPS: consecutive words of a thread that share one scale (2: group 16, 4:
 // group 32, 8: larger ones).  x3d: X as one 3-D box per stage (K a multiple of
 // 64), else one 2-D box per 64 k.  gridDim.y: CTAs (a cluster) that share an
-// item along K.
-template <int WPS, int BT>
+// item along K.  ROWS: rows of a token tile, at most.
+template <int WPS, int ROWS>
 __global__ void __launch_bounds__(THREADS, 1)
-    experts_decode_kernel(const __grid_constant__ XMaps x_maps,
+    experts_decode_kernel(const __grid_constant__ CUtensorMap x_map,
                           const __grid_constant__ CUtensorMap qw_map,
                           const __grid_constant__ CUtensorMap s_map, const int32_t* offsets,
                           uint16_t* y, int R, int K, int N, int E, int group_shift, int stages,
                           int stage_bytes, int scale_rows, int x3d, int* err) {
-  // independent accumulators: MMAs into one accumulator run one after another
-  constexpr int NACC = D_SET / BT < 4 ? D_SET / BT : 4;
-  using Table = ExpertTable<BT, 16>;
+  constexpr int BT = ROWS < 16 ? 16 : ROWS;  // MMA N
+  constexpr int ATOM_BYTES = ROWS * 128;     // X: 64-k atoms of ROWS 128-byte rows
+  constexpr int X_BYTES = 4 * ATOM_BYTES;
+  using Table = ExpertTable<ROWS, ROWS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bar = reinterpret_cast<Bars*>(ring + stages * stage_bytes);
@@ -139,14 +150,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int splits = gridDim.y;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(&bar->full[s], 1);
+    for (int s = 0; s < 2 * stages; ++s) mbar_init(&bar->full[s], 1);
+    for (int s = 0; s < stages; ++s)
       mbar_init(&bar->empty[s], 4 + 1);  // the group's warps + the MMA commit
-    }
-    for (int a = 0; a < GROUPS; ++a) {
-      mbar_init(&bar->afull[a], 4);
-      mbar_init(&bar->aempty[a], 1);
-    }
+    for (int a = 0; a < SLOTS; ++a) mbar_init(&bar->afull[a], 4);
+    for (int a = 0; a < 2 * SLOTS; ++a) mbar_init(&bar->aempty[a], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->dfull[i], 1);
       mbar_init(&bar->dempty[i], 4);
@@ -155,8 +163,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbarrier_init();
   }
   if (warp == 0 && lane == 0) {
-    prefetch_tensormap(&x_maps.rows[0]);
-    prefetch_tensormap(&x_maps.rows[1]);
+    prefetch_tensormap(&x_map);
     prefetch_tensormap(&qw_map);
     prefetch_tensormap(&s_map);
   }
@@ -182,146 +189,148 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int n_st = (int)((int64_t)(blockIdx.y + 1) * NS / splits) - st0;
 
   if (warp == 0) {
-    // ---------------- TMA producer (one lane) ----------------
-    if (lane == 0) {
-      int issued = 0, s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int j = 0; j < n_items && ok; ++j) {
-        const int item = first + j * step;
-        const ExpertTile tt = table.find(item / nblk);
-        const int n0 = (item % nblk) * BW;
-        const int big = tt.rows > X_SMALL_ROWS;
-        const CUtensorMap* xm = &x_maps.rows[big];
-        const int atom_bytes = (big ? BT : X_SMALL_ROWS) * 128;
-        for (int t = 0; t < n_st; ++t) {
-          if (!mbar_wait_bounded(&bar->empty[s], ph ^ 1u, abort_flag, kWaitLimitNs)) {
-            record_timeout(err, bar);
-            ok = false;
-            break;
-          }
+    // ---------------- TMA producer (converged; one elected lane issues) ----------------
+    int issued = 0, s = 0, v = 0;  // ring stage, and which use of it
+    bool ok = true;
+    for (int j = 0; j < n_items && ok; ++j) {
+      const int item = first + j * step;
+      const ExpertTile tt = table.find(item / nblk);
+      const int n0 = (item % nblk) * BW;
+      for (int t = 0; t < n_st; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->empty[s], (uint32_t)(v & 1) ^ 1u,
+                                                       abort_flag, kWaitLimitNs));
+        if (!ok) {
+          if (lane == 0) record_timeout(err, bar);
+          break;
+        }
+        if (elect_one()) {
           uint8_t* st = ring + s * stage_bytes;
+          uint64_t* full = &bar->full[s + stages * (v & 1)];
           const int k0 = (st0 + t) * BK;
           // 64-k atoms of X that hold k below K (a 3-D box always fills four)
           const int atoms = x3d ? 4 : min(4, (K - k0 + 63) / 64);
-          mbar_arrive_expect_tx(&bar->full[s],
-                                QW_BYTES + scale_rows * S_ROW_BYTES + atoms * atom_bytes);
-          tma_load_3d(st + BT * BK * 2, &qw_map, n0, k0 >> 3, tt.e, &bar->full[s]);
-          tma_load_3d(st + BT * BK * 2 + QW_BYTES, &s_map, n0, k0 >> gs, tt.e, &bar->full[s]);
+          mbar_arrive_expect_tx(full,
+                                QW_BYTES + scale_rows * S_ROW_BYTES + atoms * ATOM_BYTES);
+          tma_load_3d(st + X_BYTES, &qw_map, n0, k0 >> 3, tt.e, full);
+          tma_load_3d(st + X_BYTES + QW_BYTES, &s_map, n0, k0 >> gs, tt.e, full);
           if (x3d) {
-            tma_load_3d(st, xm, 0, tt.row0, k0 >> 6, &bar->full[s]);
+            tma_load_3d(st, &x_map, 0, tt.row0, k0 >> 6, full);
           } else {
             for (int a = 0; a < atoms; ++a)
-              tma_load_2d(st + a * atom_bytes, xm, k0 + 64 * a, tt.row0, &bar->full[s]);
-          }
-          ++issued;
-          if (++s == stages) {
-            s = 0;
-            ph ^= 1u;
+              tma_load_2d(st + a * ATOM_BYTES, &x_map, k0 + 64 * a, tt.row0, full);
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++s == stages) {
+          s = 0;
+          ++v;
+        }
       }
-      if (*abort_flag) {
-        // drain: wait (bounded) for the last load issued into each slot
-        int never = 0;
-        for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
-          mbar_wait_bounded(&bar->full[i % stages], (uint32_t)(i / stages) & 1u, &never,
-                            kDrainLimitNs);
-      }
-      // all copies are issued: the next kernel in the stream may start its
-      // prologue (it waits for this grid before touching its inputs)
-      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
+    if (*abort_flag) {
+      // drain: wait (bounded) for the last load issued into each slot
+      int never = 0;
+      for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
+        mbar_wait_bounded(&bar->full[i % (2 * stages)], (uint32_t)(i / (2 * stages)) & 1u, &never,
+                          kDrainLimitNs);
+    }
+    // all copies are issued: the next kernel in the stream may start its
+    // prologue (it waits for this grid before touching its inputs)
+    if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer (converged; one elected lane issues) ----------------
+    constexpr uint32_t idesc = idesc_f16_f32(BW, BT);
     bool ok = true;
-    int s = 0, a = 0, j = 0;
-    uint32_t ph = 0, aph = 0;
-    for (; j < n_items && ok; ++j) {
-      const ExpertTile tt = table.find((first + j * step) / nblk);
-      const uint32_t idesc = idesc_f16_f32(BW, tt.n);
-      const uint32_t atom_bytes = (tt.rows > X_SMALL_ROWS ? BT : X_SMALL_ROWS) * 128;
-      const uint32_t d_base = tmem + D_COL + (uint32_t)(j & 1) * D_SET;
+    int s = 0, a = 0, use = 0;
+    for (int j = 0; j < n_items && ok; ++j) {
+      const uint32_t d = tmem + D_COL + (uint32_t)(j & 1) * D_NEXT;
       if (j >= 2) {
         ok = __all_sync(0xffffffffu,
                         mbar_wait_bounded(&bar->dempty[j & 1], (uint32_t)((j - 2) >> 1) & 1u,
                                           abort_flag, kWaitLimitNs));
         if (!ok) break;
-        tc_fence_after();
       }
       for (int t = 0; t < n_st; ++t) {
+        // the stage's X has landed too: its A slot was written from the stage
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&bar->full[s], ph, abort_flag, kWaitLimitNs) &&
-                            mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs));
+                        mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag,
+                                          kWaitLimitNs));
         if (!ok) break;
         tc_fence_after();
         const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
         const uint32_t a_base = tmem + A_COL + a * A_SLOT_COLS;
         const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
+        const uint32_t keep = t > 0 ? 1u : 0u;
         if (elect_one()) {
+          if (nk == BK / 16) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            if (kk < nk)
-              mma_f16_ts(d_base + (kk % NACC) * BT, a_base + 8 * kk,
-                         x_desc + (uint64_t)(((kk >> 2) * atom_bytes + (kk & 3) * 32) >> 4),
-                         idesc, t > 0 || kk >= NACC ? 1u : 0u);
-          mma_commit(&bar->aempty[a]);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_f16_ts(d, a_base + 8 * kk,
+                         x_desc + (uint64_t)(((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4),
+                         idesc, kk > 0 ? 1u : keep);
+          } else {
+#pragma unroll 1
+            for (int kk = 0; kk < nk; ++kk)
+              mma_f16_ts(d, a_base + 8 * kk,
+                         x_desc + (uint64_t)(((kk >> 2) * ATOM_BYTES + (kk & 3) * 32) >> 4),
+                         idesc, kk > 0 ? 1u : keep);
+          }
+          mma_commit(&bar->aempty[a + SLOTS * (use & 1)]);
           mma_commit(&bar->empty[s]);
           if (t == n_st - 1) mma_commit(&bar->dfull[j & 1]);
         }
         __syncwarp();
-        if (++a == GROUPS) {
+        if (++a == SLOTS) {
           a = 0;
-          aph ^= 1u;
+          ++use;
         }
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1u;
-        }
+        if (++s == stages) s = 0;
       }
     }
     if (!ok) {
       if (lane == 0) record_timeout(err, bar);
       // wait (bounded) for the MMAs already issued before TMEM is freed
-      if (elect_one()) mma_commit(&bar->aempty[a]);
+      uint64_t* last = &bar->aempty[a + SLOTS * (use & 1)];
+      if (elect_one()) mma_commit(last);
       __syncwarp();
       int never = 0;
-      mbar_wait_bounded(&bar->aempty[a], aph, &never, kDrainLimitNs);
+      mbar_wait_bounded(last, (uint32_t)(use >> 1) & 1u, &never, kDrainLimitNs);
     }
     __syncwarp();
   } else if (warp < EPI_WARP0) {
     // ---------------- dequantisation ----------------
-    const int grp = (warp - DQ_WARP0) >> 2;  // stages t = grp mod GROUPS, A slot grp
+    const int grp = (warp - DQ_WARP0) >> 2;
     const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
     const int col = 32 * quarter + lane;
     const int gid = ((warp - DQ_WARP0) & 3) * 32 + lane;
-    const uint32_t a_slot = tmem + ((uint32_t)(32 * quarter) << 16) + A_COL + grp * A_SLOT_COLS;
+    const uint32_t a_lane = tmem + ((uint32_t)(32 * quarter) << 16) + A_COL;
     const int total = n_items * n_st;
-    int s = grp % stages;
-    uint32_t ph = (uint32_t)(grp / stages) & 1u, aph = 0;
+    int s = grp % stages, v = grp / stages;        // ring stage, and which use of it
+    int a = grp % SLOTS, use = grp / SLOTS;  // A slot, and which use of it
     int j = -1, t = grp - GROUPS;  // item, and stage in it
-    int rows = 0, atom_bytes = 0;
+    int rows = 0;
     bool ok = true;
     for (int f = grp; f < total; f += GROUPS) {
       t += GROUPS;
       while (j < 0 || t >= n_st) {
         if (j >= 0) t -= n_st;
         ++j;
-        const ExpertTile tt = table.find((first + j * step) / nblk);
-        rows = tt.rows;
-        atom_bytes = (tt.rows > X_SMALL_ROWS ? BT : X_SMALL_ROWS) * 128;
+        rows = table.find((first + j * step) / nblk).rows;
       }
       const int k_left = K - (st0 + t) * BK;  // k below K from the stage's first on
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->full[s], ph, abort_flag, kWaitLimitNs));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->full[s + stages * (v & 1)],
+                                                     (uint32_t)(v >> 1) & 1u, abort_flag,
+                                                     kWaitLimitNs));
       if (!ok) break;
       uint8_t* st = ring + s * stage_bytes;
       // 32 chunks per row and stage: chunk c of 64-k atom c / 8 (every chunk of
       // a row is permuted, so the swizzle does not matter)
       for (int i = gid; i < 32 * rows; i += 128)
-        permute_x_chunk(st + ((i & 31) >> 3) * atom_bytes + (i >> 5) * 128 + (i & 7) * 16);
-      const uint8_t* qw = st + BT * BK * 2 + col * 4;
-      const uint8_t* sc = st + BT * BK * 2 + QW_BYTES + col * 2;
+        permute_x_chunk(st + ((i & 31) >> 3) * ATOM_BYTES + (i >> 5) * 128 + (i & 7) * 16);
+      const uint8_t* qw = st + X_BYTES + col * 4;
+      const uint8_t* sc = st + X_BYTES + QW_BYTES + col * 2;
 #pragma unroll
       for (int c = 0; c < PR / WPT; ++c) {
         uint32_t cells[4 * WPT];
@@ -355,24 +364,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (c == 0) {
           // the A slot is free once the MMAs of its previous use have completed
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->aempty[grp], aph ^ 1u, abort_flag,
-                                                         kWaitLimitNs));
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar->aempty[a + SLOTS * ((use - 1) & 1)],
+                                            (uint32_t)((use - 1) >> 1) & 1u, abort_flag,
+                                            kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
         }
-        if (64 * c < k_left) tmem_st_32x32b_x32(a_slot + 4 * WPT * c, cells);
+        if (64 * c < k_left) tmem_st_32x32b_x32(a_lane + a * A_SLOT_COLS + 4 * WPT * c, cells);
       }
       if (!ok) break;
       tmem_wait_st();
       fence_proxy_async_smem();  // the permuted X rows, for the MMAs
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->afull[grp]);
-      aph ^= 1u;
+      if (lane == 0) mbar_arrive(&bar->afull[a]);
+      a += GROUPS % SLOTS;
+      use += GROUPS / SLOTS;
+      if (a >= SLOTS) {
+        a -= SLOTS;
+        ++use;
+      }
       s += GROUPS;
       if (s >= stages) {
         s -= stages;
-        ph ^= 1u;
+        ++v;
       }
     }
     if (!ok && lane == 0) record_timeout(err, bar);
@@ -383,8 +399,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int col = 32 * quarter + lane;
     const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
     float* part = reinterpret_cast<float*>(ring);  // [token][column], splits > 1
-    // accumulators that hold something (fewer when K ends within the first)
-    const int nacc = min(NACC, (K - st0 * BK) / 16);
     for (int j = 0; j < n_items; ++j) {
       const int item = first + j * step;
       const ExpertTile tt = table.find(item / nblk);
@@ -396,28 +410,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t d_set = tmem + lane_addr + D_COL + (uint32_t)(j & 1) * D_SET;
+      const uint32_t d = tmem + lane_addr + D_COL + (uint32_t)(j & 1) * D_NEXT;
       uint16_t* out = y + (int64_t)tt.row0 * N + n;
+      const int blocks = (tt.rows + 15) / 16;
 #pragma unroll 1
-      for (int tb = 0; tb < tt.n / 16; ++tb) {
-        // the block's accumulators requested at once, summed in a fixed order
-        uint32_t v[NACC][16];
-#pragma unroll
-        for (int c = 0; c < NACC; ++c) tmem_ld_32x32b_x16(d_set + c * BT + 16 * tb, v[c]);
+      for (int tb = 0; tb < blocks; ++tb) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(d + 16 * tb, v);
         tmem_wait_ld();
-        if (16 * (tb + 1) == tt.n) {
+        if (tb == blocks - 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->dempty[j & 1]);  // the set may be overwritten
+          if (lane == 0) mbar_arrive(&bar->dempty[j & 1]);  // it may be overwritten
         }
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          float acc = __uint_as_float(v[0][q]);
-#pragma unroll
-          for (int c = 1; c < NACC; ++c)
-            if (c < nacc) acc += __uint_as_float(v[c][q]);
+          const float acc = __uint_as_float(v[q]);
           const int tok = 16 * tb + q;
-          if (splits > 1)
+          if (splits > 1 && tok < tt.rows)
             part[tok * BW + col] = acc;
           else if (tok < tt.rows && n < N)
             out[(int64_t)tok * N] = __half_as_ushort(__float2half_rn(acc));
@@ -455,8 +465,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int WPS, int BT>
-cudaError_t launch_t(const XMaps& x_maps, const CUtensorMap& qw_map, const CUtensorMap& s_map,
+template <int WPS, int ROWS>
+cudaError_t launch_t(const CUtensorMap& x_map, const CUtensorMap& qw_map, const CUtensorMap& s_map,
                      const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
                      int64_t E, int group_shift, const Shape& d, int x3d, int64_t items,
                      int splits, cudaStream_t stream, const DeviceInfo& dev) {
@@ -464,7 +474,7 @@ cudaError_t launch_t(const XMaps& x_maps, const CUtensorMap& qw_map, const CUten
   static cudaError_t attr_err[64];
   const int di = dev.device & 63;
   std::call_once(once[di], [&] {
-    attr_err[di] = cudaFuncSetAttribute(experts_decode_kernel<WPS, BT>,
+    attr_err[di] = cudaFuncSetAttribute(experts_decode_kernel<WPS, ROWS>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         1024 + kSmemLimit);
   });
@@ -484,7 +494,7 @@ cudaError_t launch_t(const XMaps& x_maps, const CUtensorMap& qw_map, const CUten
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, experts_decode_kernel<WPS, BT>, x_maps, qw_map, s_map, offsets,
+  return cudaLaunchKernelEx(&cfg, experts_decode_kernel<WPS, ROWS>, x_map, qw_map, s_map, offsets,
                             y, (int)R, (int)K, (int)N, (int)E, group_shift, d.stages,
                             d.stage_bytes, d.scale_rows, x3d, dev.error_word);
 }
@@ -499,28 +509,24 @@ int pick_splits(int64_t items, int64_t K, const DeviceInfo& dev) {
   return s < 1 ? 1 : (int)s;
 }
 
-template <int BT>
-cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+template <int ROWS>
+cudaError_t launch_rows(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
                       const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
                       int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
-  const Shape d = shape_of<BT>(group_shift, (int)E);
+  const Shape d = shape_of<ROWS>(group_shift, (int)E);
   if (d.stages < GROUPS) return cudaErrorInvalidValue;
   const int64_t n_groups = (group_shift == 62 || (int64_t(1) << group_shift) >= K)
                                ? 1 : (K + (int64_t(1) << group_shift) - 1) >> group_shift;
-  XMaps x_maps;
-  CUtensorMap qw_map, s_map;
+  CUtensorMap x_map, qw_map, s_map;
   const int x3d = K % 64 == 0;
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t rows = i ? BT : X_SMALL_ROWS;
-    const uint64_t dims[3] = {64, (uint64_t)R, (uint64_t)(K / 64)};
-    const uint64_t strides[2] = {(uint64_t)K * 2, 128};
-    const uint32_t box[3] = {64, rows, BK / 64};
-    if (!(x3d ? encode_map_3d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides,
-                              box, CU_TENSOR_MAP_SWIZZLE_128B)
-              : encode_map_2d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)K,
-                              (uint64_t)R, (uint64_t)K * 2, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B)))
-      return cudaErrorInvalidValue;
-  }
+  const uint64_t dims[3] = {64, (uint64_t)R, (uint64_t)(K / 64)};
+  const uint64_t strides[2] = {(uint64_t)K * 2, 128};
+  const uint32_t box[3] = {64, ROWS, BK / 64};
+  if (!(x3d ? encode_map_3d(&x_map, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides, box,
+                            CU_TENSOR_MAP_SWIZZLE_128B)
+            : encode_map_2d(&x_map, x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)K, (uint64_t)R,
+                            (uint64_t)K * 2, 64, ROWS, CU_TENSOR_MAP_SWIZZLE_128B)))
+    return cudaErrorInvalidValue;
   const uint64_t qdims[3] = {(uint64_t)N, (uint64_t)(K / 8), (uint64_t)E};
   const uint64_t qstrides[2] = {(uint64_t)N * 4, (uint64_t)(K / 8) * N * 4};
   const uint32_t qbox[3] = {BW, PR, 1};
@@ -533,14 +539,14 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
                      CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   // the most items there can be: a tile per row, or one per expert and one
-  // more for every BT / 2 rows beyond that (tiles are at least half full)
-  const int64_t tiles = std::min<int64_t>(R, E + R / (BT / 2));
+  // more for every ROWS rows beyond that
+  const int64_t tiles = std::min<int64_t>(R, E + R / ROWS);
   const int64_t items = tiles * ((N + BW - 1) / BW);
   const int splits = pick_splits(items, K, dev);
-  const auto launch = group_shift == 4   ? launch_t<2, BT>
-                      : group_shift == 5 ? launch_t<4, BT>
-                                         : launch_t<WPT, BT>;
-  return launch(x_maps, qw_map, s_map, offsets, y, R, K, N, E, group_shift, d, x3d, items, splits,
+  const auto launch = group_shift == 4   ? launch_t<2, ROWS>
+                      : group_shift == 5 ? launch_t<4, ROWS>
+                                         : launch_t<WPT, ROWS>;
+  return launch(x_map, qw_map, s_map, offsets, y, R, K, N, E, group_shift, d, x3d, items, splits,
                 stream, dev);
 }
 
@@ -550,7 +556,10 @@ cudaError_t launch_experts_decode(const uint16_t* x, const int32_t* qweight,
                                   const uint16_t* scales, const int32_t* offsets, uint16_t* y,
                                   int64_t R, int64_t K, int64_t N, int64_t E, int group_shift,
                                   int tile, cudaStream_t stream, const DeviceInfo& dev) {
-  const auto launch = tile <= 16 ? launch_bt<16> : tile <= 32 ? launch_bt<32> : launch_bt<64>;
+  const auto launch = tile <= 8    ? launch_rows<8>
+                      : tile <= 16 ? launch_rows<16>
+                      : tile <= 32 ? launch_rows<32>
+                                   : launch_rows<64>;
   return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
 }
 

@@ -264,7 +264,7 @@ DECODE = [  # more for the kernel of few rows: (rows per expert, K, N, G, rows b
 
 @pytest.mark.parametrize("case", PRODUCT + DECODE,
                          ids=lambda c: f"E{len(c[0])}-K{c[1]}-N{c[2]}-G{c[3]}")
-@pytest.mark.parametrize("tile", [16, 32, 64])
+@pytest.mark.parametrize("tile", [8, 16, 32, 64])
 def test_product_of_few_rows(case, tile):
     counts, K, N, G, tail = case
     rows, q, s, offsets = product_inputs(case, False)
@@ -279,6 +279,29 @@ def test_product_of_few_rows(case, tile):
            f"tile {tile} E={len(counts)} K={K} N={N} G={G}")
     again = B.gemm_experts(*args, kernel=B.KERNEL_DECODE, tile=tile).cpu().numpy()
     assert np.array_equal(bits(again[:live]), bits(got[:live]))
+
+
+@pytest.mark.parametrize("tile", [8, 16, 32, 64])
+def test_few_rows_over_long_walks(tile):
+    """Many items and stages per CTA, over and over: the ring, the A slots and
+    the accumulators wrap around many times, with the same result each time
+    and the other kernel's within the bound."""
+    rng = np.random.default_rng(tile)
+    K, N, G, E = 2048, 2048, 128, 48
+    offsets = P.offsets_of(rng.integers(0, 2 * tile // 3 + 3, E))
+    x, (q, s) = P.make_rows(rng, int(offsets[-1]), K), P.make_weights(rng, E, K, N, G)
+    args = (cu(x), cu(q), cu(s), cu(offsets), G)
+    first = B.gemm_experts(*args, kernel=B.KERNEL_DECODE, tile=tile)
+    for _ in range(30):
+        assert torch.equal(B.gemm_experts(*args, kernel=B.KERNEL_DECODE, tile=tile), first)
+    assert B.device_error() == 0
+    some = rng.choice(len(x), 24, replace=False)
+    expert = np.searchsorted(offsets, some, side="right") - 1
+    for r, e in zip(some, expert):
+        w = oracle.dequant(q[e], s[e], G).astype(np.float64)
+        ref = x[r].astype(np.float64) @ w
+        size = np.abs(x[r].astype(np.float64)) @ np.abs(w)
+        within(first[r].cpu().numpy(), ref, P.product_tol(ref, size, K), f"tile {tile} row {r}")
 
 
 @pytest.mark.parametrize("counts", [[2, 3, 1], [40, 70, 20], [300, 5, 140]])
@@ -300,7 +323,7 @@ def test_one_hot_rows_reproduce_weights(counts, G):
     R = int(offsets[-1])
     expert = np.searchsorted(offsets, np.arange(R), side="right") - 1
     keep = expert != 1
-    decode = [dict(kernel=B.KERNEL_DECODE, tile=t) for t in (16, 32, 64)]
+    decode = [dict(kernel=B.KERNEL_DECODE, tile=t) for t in (8, 16, 32, 64)]
     for kw in [{}, dict(kernel=B.KERNEL_PREFILL), *decode, None]:
         gradient = kw is None
         width = N if gradient else K
