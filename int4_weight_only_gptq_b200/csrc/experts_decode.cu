@@ -114,6 +114,12 @@ Shape shape_of(int group_shift, int E) {
   return d;
 }
 
+// A value that every lane of the warp holds, in a form that the compiler knows
+// to be warp-uniform (a warp reduction): loop bounds and addresses read from
+// shared memory, on which the issuing warps' descriptors depend, would keep
+// those out of the uniform datapath otherwise.
+__device__ __forceinline__ int uniform(int v) { return (int)__reduce_max_sync(0xffffffffu, v); }
+
 // One 16-byte chunk of an X row (eight consecutive k) rewritten in place from
 // natural order to the paired order of the unpacked weights.
 __device__ __forceinline__ void permute_x_chunk(uint8_t* p) {
@@ -124,6 +130,48 @@ __device__ __forceinline__ void permute_x_chunk(uint8_t* p) {
   o.z = prmt(v.y, v.w, 0x5410);
   o.w = prmt(v.y, v.w, 0x7632);
   *reinterpret_cast<uint4*>(p) = o;
+}
+
+// One stage's 32 words of a thread's column into its 128 TMEM cells of an A
+// slot: eight words at a time, the next eight under way meanwhile.  SMALL: the
+// scales allow the form with fewer operations (same values; every lane of the
+// warp).  `ready` waits for the slot, after the first eight words are done.
+template <int WPS, bool SMALL, class Ready>
+__device__ __forceinline__ bool dequant_stage(const uint8_t* qw, const uint8_t* sc, int gs,
+                                              uint32_t a_cells, Ready ready) {
+  uint32_t w[2][WPT];
+#pragma unroll
+  for (int i = 0; i < WPT; ++i) w[0][i] = *reinterpret_cast<const uint32_t*>(qw + i * QW_ROW_BYTES);
+#pragma unroll
+  for (int c = 0; c < PR / WPT; ++c) {
+    if (c + 1 < PR / WPT) {
+#pragma unroll
+      for (int i = 0; i < WPT; ++i)
+        w[(c + 1) & 1][i] =
+            *reinterpret_cast<const uint32_t*>(qw + (WPT * (c + 1) + i) * QW_ROW_BYTES);
+    }
+    uint32_t cells[4 * WPT];
+#pragma unroll
+    for (int g = 0; g < WPT / WPS; ++g) {
+      const int srow = (8 * (WPT * c + WPS * g)) >> gs;
+      const uint32_t s2 =
+          half2_broadcast(*reinterpret_cast<const uint16_t*>(sc + srow * S_ROW_BYTES));
+      uint32_t b2, c2;
+      if (SMALL) subnormal_form_constants(s2, b2, c2);
+#pragma unroll
+      for (int i = 0; i < WPS; ++i) {
+        const uint32_t word = w[c & 1][WPS * g + i];
+        uint32_t* out = cells + 4 * (WPS * g + i);
+        if (SMALL)
+          dequant_word_paired_small_scale(word, s2, b2, c2, out);
+        else
+          dequant_word_paired(word, s2, out);
+      }
+    }
+    if (c == 0 && !ready()) return false;
+    tmem_st_32x32b_x32(a_cells + 4 * WPT * c, cells);
+  }
+  return true;
 }
 
 // WPS: consecutive words of a thread that share one scale (2: group 16, 4:
@@ -190,12 +238,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ---------------- TMA producer (converged; one elected lane issues) ----------------
+    const int count = uniform(n_items);
     int issued = 0, s = 0, v = 0;  // ring stage, and which use of it
     bool ok = true;
-    for (int j = 0; j < n_items && ok; ++j) {
+    for (int j = 0; j < count && ok; ++j) {
       const int item = first + j * step;
       const ExpertTile tt = table.find(item / nblk);
-      const int n0 = (item % nblk) * BW;
+      const int n0 = (item % nblk) * BW, e = uniform(tt.e), row0 = uniform(tt.row0);
       for (int t = 0; t < n_st; ++t) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->empty[s], (uint32_t)(v & 1) ^ 1u,
                                                        abort_flag, kWaitLimitNs));
@@ -211,13 +260,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int atoms = x3d ? 4 : min(4, (K - k0 + 63) / 64);
           mbar_arrive_expect_tx(full,
                                 QW_BYTES + scale_rows * S_ROW_BYTES + atoms * ATOM_BYTES);
-          tma_load_3d(st + X_BYTES, &qw_map, n0, k0 >> 3, tt.e, full);
-          tma_load_3d(st + X_BYTES + QW_BYTES, &s_map, n0, k0 >> gs, tt.e, full);
+          tma_load_3d(st + X_BYTES, &qw_map, n0, k0 >> 3, e, full);
+          tma_load_3d(st + X_BYTES + QW_BYTES, &s_map, n0, k0 >> gs, e, full);
           if (x3d) {
-            tma_load_3d(st, &x_map, 0, tt.row0, k0 >> 6, full);
+            tma_load_3d(st, &x_map, 0, row0, k0 >> 6, full);
           } else {
             for (int a = 0; a < atoms; ++a)
-              tma_load_2d(st + a * ATOM_BYTES, &x_map, k0 + 64 * a, tt.row0, full);
+              tma_load_2d(st + a * ATOM_BYTES, &x_map, k0 + 64 * a, row0, full);
           }
         }
         __syncwarp();
@@ -242,10 +291,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (converged; one elected lane issues) ----------------
     constexpr uint32_t idesc = idesc_f16_f32(BW, BT);
+    const int count = uniform(n_items);
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
     bool ok = true;
     int s = 0, a = 0, use = 0;
-    for (int j = 0; j < n_items && ok; ++j) {
-      const uint32_t d = tmem + D_COL + (uint32_t)(j & 1) * D_NEXT;
+    for (int j = 0; j < count && ok; ++j) {
+      const uint32_t d = tm + D_COL + (uint32_t)(j & 1) * D_NEXT;
       if (j >= 2) {
         ok = __all_sync(0xffffffffu,
                         mbar_wait_bounded(&bar->dempty[j & 1], (uint32_t)((j - 2) >> 1) & 1u,
@@ -260,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
-        const uint32_t a_base = tmem + A_COL + a * A_SLOT_COLS;
+        const uint32_t a_base = tm + A_COL + a * A_SLOT_COLS;
         const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
         const uint32_t keep = t > 0 ? 1u : 0u;
         if (elect_one()) {
@@ -319,7 +370,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++j;
         rows = table.find((first + j * step) / nblk).rows;
       }
-      const int k_left = K - (st0 + t) * BK;  // k below K from the stage's first on
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->full[s + stages * (v & 1)],
                                                      (uint32_t)(v >> 1) & 1u, abort_flag,
                                                      kWaitLimitNs));
@@ -331,48 +381,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         permute_x_chunk(st + ((i & 31) >> 3) * ATOM_BYTES + (i >> 5) * 128 + (i & 7) * 16);
       const uint8_t* qw = st + X_BYTES + col * 4;
       const uint8_t* sc = st + X_BYTES + QW_BYTES + col * 2;
+      // the A slot is free once the MMAs of its previous use have completed
+      const auto ready = [&]() -> bool {
+        const bool free =
+            __all_sync(0xffffffffu, mbar_wait_bounded(&bar->aempty[a + SLOTS * ((use - 1) & 1)],
+                                                      (uint32_t)((use - 1) >> 1) & 1u, abort_flag,
+                                                      kWaitLimitNs));
+        tc_fence_after();
+        return free;
+      };
+      // one form for the whole stage, so that its branch is the warp's
+      bool small = WPS >= 4;
+      if (WPS >= 4) {
 #pragma unroll
-      for (int c = 0; c < PR / WPT; ++c) {
-        uint32_t cells[4 * WPT];
-        if (64 * c < k_left) {
-#pragma unroll
-          for (int g = 0; g < WPT / WPS; ++g) {
-            const int r0 = WPT * c + WPS * g;
-            const int srow = (8 * r0) >> gs;
-            const uint32_t s2 =
-                half2_broadcast(*reinterpret_cast<const uint16_t*>(sc + srow * S_ROW_BYTES));
-            uint32_t w[WPS];
-#pragma unroll
-            for (int i = 0; i < WPS; ++i)
-              w[i] = *reinterpret_cast<const uint32_t*>(qw + (r0 + i) * QW_ROW_BYTES);
-            if (WPS >= 4 && scale_fits_subnormal_form(s2)) {
-              uint32_t b2, c2;
-              subnormal_form_constants(s2, b2, c2);
-#pragma unroll
-              for (int i = 0; i < WPS; ++i)
-                dequant_word_paired_small_scale(w[i], s2, b2, c2, cells + 4 * (WPS * g + i));
-            } else {
-#pragma unroll
-              for (int i = 0; i < WPS; ++i)
-                dequant_word_paired(w[i], s2, cells + 4 * (WPS * g + i));
-            }
-          }
-        }
-        if (c == PR / WPT - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->empty[s]);  // qweight and scales of the stage read
-        }
-        if (c == 0) {
-          // the A slot is free once the MMAs of its previous use have completed
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar->aempty[a + SLOTS * ((use - 1) & 1)],
-                                            (uint32_t)((use - 1) >> 1) & 1u, abort_flag,
-                                            kWaitLimitNs));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        if (64 * c < k_left) tmem_st_32x32b_x32(a_lane + a * A_SLOT_COLS + 4 * WPT * c, cells);
+        for (int g = 0; g < PR / WPS; ++g)
+          small = small && scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
+                               sc + ((8 * WPS * g) >> gs) * S_ROW_BYTES));
+        small = __all_sync(0xffffffffu, small);
       }
+      const uint32_t a_cells = a_lane + a * A_SLOT_COLS;
+      ok = small ? dequant_stage<WPS, true>(qw, sc, gs, a_cells, ready)
+                 : dequant_stage<WPS, false>(qw, sc, gs, a_cells, ready);
+      // qweight and scales of the stage are read (a lane's words were used
+      // before it got here)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->empty[s]);
       if (!ok) break;
       tmem_wait_st();
       fence_proxy_async_smem();  // the permuted X rows, for the MMAs
