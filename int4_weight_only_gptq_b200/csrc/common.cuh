@@ -132,6 +132,19 @@ __device__ __forceinline__ void dequant_word_paired_small_scale(uint32_t w, uint
   p[3] = hfma2_rn(and_b32(w8, 0x00F000F0u), b2, c2);
 }
 
+// Natural k order for a scale with 0 < s < 2^-4 (b2, c2 from
+// subnormal_form_constants): byte j of the word holds codes k_{2j} (low
+// nibble) and k_{2j+1}; taken from w << 4 and from w, both lie at bits 4..7 of
+// their half, as the subnormals q * 2^-20.  13 operations a word, 17 without.
+__device__ __forceinline__ void dequant_word_natural_small_scale(uint32_t w, uint32_t b2,
+                                                                 uint32_t c2, uint32_t n[4]) {
+  const uint32_t w4 = w << 4;
+  n[0] = hfma2_rn(and_b32(prmt(w4, w, 0x4400), 0x00F000F0u), b2, c2);
+  n[1] = hfma2_rn(and_b32(prmt(w4, w, 0x5511), 0x00F000F0u), b2, c2);
+  n[2] = hfma2_rn(and_b32(prmt(w4, w, 0x6622), 0x00F000F0u), b2, c2);
+  n[3] = hfma2_rn(and_b32(prmt(w4, w, 0x7733), 0x00F000F0u), b2, c2);
+}
+
 // Same, in natural k order: n[j] = (k_{2j}, k_{2j+1}).
 __device__ __forceinline__ void dequant_word_natural(uint32_t w, uint32_t s2, uint32_t n[4]) {
   uint32_t p[4];

@@ -12,21 +12,29 @@
 // * The experts' row counts are known on the device only.  Every CTA builds
 //   the same table of token tiles from the offsets (experts.cuh) and cluster c
 //   takes tiles c, c + clusters, ..., column pair fastest.
-// * A tile holds up to 256 rows of one expert; the MMA's width is the rows
-//   rounded up to 32, so an expert with few rows pays for those only.  The
-//   copy boxes of X come in 32, 64 and 128 rows per CTA for the same reason.
-//   Rows that a box reads past the tile belong to other experts (or read as
-//   zero past the tensor): each is a column of the accumulator of its own,
-//   which is never stored.
-// * Stores: 64-row blocks wholly inside the tile go through TMA, the others
+// * A tile holds up to BT = 128 or 256 rows of one expert; the MMA's width is
+//   the rows rounded up to 32, so an expert with few rows pays for those only.
+//   The copy boxes of X come in 32, 64 and 128 rows per CTA for the same
+//   reason.  Rows that a box reads past the tile belong to other experts (or
+//   read as zero past the tensor): each is a column of the accumulator of its
+//   own, which is never stored.
+// * Four warps of their own read a finished accumulator out.  Tiles of up to
+//   128 rows alternate between the two halves of the accumulator columns, so
+//   the next tile's MMAs run meanwhile: with few rows per expert a tile takes
+//   a few microseconds, and waiting for its read-out took a fifth of them.
+// * Stores: 32-row blocks wholly inside the tile go through TMA, the others
 //   as 16-byte rows, so that no other expert's row is written.
 //
 // In the gradient the roles of K and N are exchanged: the pair's 256 columns
 // are k, the contraction runs over n.  The weight tile of a stage is the same
-// box of 16 packed rows x 128 columns, but a TMEM lane is now one k: its
-// thread reads every word of its packed row, picks its own nibble of two
-// neighbouring words with one byte permute, and multiplies them by the two
-// columns' scales.
+// box of 16 packed rows x 128 columns, but a TMEM lane is now one k.  A thread
+// takes half a packed word (four k) of four neighbouring columns at a time:
+// one byte permute collects a byte of two columns' words, whose two nibbles
+// are two k of that column pair.  Stored in the 16-lane, 256-bit form of
+// tcgen05.st, a thread's four k lie in TMEM lanes r, r + 8, r + 16 and r + 24
+// of its quarter: lane l holds k = 4 (l mod 8) + l / 8, which the read-out
+// undoes.  (With a lane per thread, every word was read by eight threads and
+// shared memory bound the kernel.)
 //
 // Every wait is bounded in time; on expiry the CTA records GPTQ_ERR_TIMEOUT
 // in the device error word and winds down.  Both CTAs always reach the final
@@ -51,29 +59,30 @@ namespace {
 
 constexpr int BW = 128;   // output columns per CTA (TMEM lanes); 256 per pair (MMA M)
 constexpr int BK = 128;   // contraction per pipeline stage (eight k16 MMAs)
-constexpr int BT = 256;   // tokens per pair tile, at most
-constexpr int HT = BT / 2;  // ... loaded by each CTA
-constexpr int XS = 3;     // X ring stages (half tile per CTA)
-constexpr int WS = 4;     // weight-tile ring stages (qweight + scales)
+constexpr int XS_MAX = 6;  // X ring stages, at most
+constexpr int WS = 8;     // weight-tile ring stages (qweight + scales)
 constexpr int AS = 4;     // A slots in TMEM (BK each)
 constexpr int DQ_GROUPS = 4;             // dequantisation groups: group g takes stages g mod 4
 constexpr int DQ_WARPS = 4 * DQ_GROUPS;  // one warp per TMEM lane quarter in each group
 constexpr int DQ_WARP0 = 3;  // warps 0, 1, 2: X producer, MMA issuer, weight producer
-constexpr int THREADS = (DQ_WARP0 + DQ_WARPS) * 32;
+constexpr int EPI_WARP0 = DQ_WARP0 + DQ_WARPS;  // four read-out warps
+constexpr int THREADS = (EPI_WARP0 + 4) * 32;
 constexpr int QW_STAGE_BYTES = BW * (BK / 8) * 4;  // 16 packed rows x 128 columns: 8 KB
 constexpr int QW_ROW_BYTES = BW * 4;
 constexpr int S_ROW_BYTES = BW * 2;                // one scale row of the tile: 256 B
 constexpr int S_STAGE_MAX_ROWS = BK / 16;          // group 16: eight rows per stage
 constexpr int W_STAGE_BYTES = QW_STAGE_BYTES + S_STAGE_MAX_ROWS * S_ROW_BYTES;
-constexpr int X_STAGE_BYTES = 2 * HT * 128;        // two 64-k halves of 128-byte rows
-constexpr int TPG = BT / DQ_GROUPS;                // tokens read out per group
-constexpr int Y_WARP_BYTES = TPG * 32 * 2;         // a warp's staging block: 64 tokens x 32 columns
-constexpr int W_OFF = XS * X_STAGE_BYTES;
+constexpr int X_RING_BYTES = 96 * 1024;            // three stages of 256 tokens, six of 128
+constexpr int Y_ROWS = 32;                         // tokens per store block
+constexpr int Y_BLOCK_BYTES = Y_ROWS * 32 * 2;     // ... of a read-out warp's 32 columns
+constexpr int Y_BLOCKS = 2;                        // per read-out warp, in turn
+constexpr int W_OFF = X_RING_BYTES;
 constexpr int Y_OFF = W_OFF + WS * W_STAGE_BYTES;
-constexpr int BAR_OFF = Y_OFF + DQ_WARPS * Y_WARP_BYTES;
+constexpr int BAR_OFF = Y_OFF + 4 * Y_BLOCKS * Y_BLOCK_BYTES;
 constexpr int TABLE_OFF = BAR_OFF + 512;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t D_COL = 0;              // accumulator: columns [0, BT)
+constexpr uint32_t D_COL = 0;              // accumulators: columns [0, 256)
+constexpr uint32_t D_HALF = 128;           // ... tiles of up to 128 rows alternate
 constexpr uint32_t A_COL = 256;            // A slots: [256, 256 + 4 * 64)
 constexpr uint32_t A_STAGE_COLS = BK / 2;  // two FP16 per 32-bit column
 constexpr uint16_t kPairMask = 0x3;        // both CTAs of the cluster
@@ -83,21 +92,27 @@ static_assert(A_COL + AS * A_STAGE_COLS <= TMEM_COLS, "TMEM budget");
 static_assert(AS == DQ_GROUPS && WS % DQ_GROUPS == 0,
               "stage g uses A slot g mod 4 and weight slot g mod WS, both of group g mod 4");
 
-using Table = ExpertTable<BT, 32>;
-static_assert(1024 + TABLE_OFF + Table::bytes(GPTQ_MOE_MAX_EXPERTS) <= 227 * 1024,
+template <int BT>
+struct Geo {
+  using Table = ExpertTable<BT, 32>;
+  static constexpr int X_STAGE_BYTES = BT * 128;  // two 64-column halves of BT / 2 rows
+  static constexpr int XS = X_RING_BYTES / X_STAGE_BYTES;
+  static_assert(XS <= XS_MAX, "X ring stages");
+};
+static_assert(1024 + TABLE_OFF + ExpertTable<256, 32>::bytes(GPTQ_MOE_MAX_EXPERTS) <= 227 * 1024,
               "shared memory per CTA");
 
 // Both CTAs hold the full set; xfull, afull and dempty are only used in the
-// even CTA.
+// even CTA.  dfull and dempty of tile i: entry i mod 2.
 struct PairBarriers {
-  uint64_t xfull[XS];   // both halves of the X stage landed (even CTA)
-  uint64_t xempty[XS];  // pair MMAs reading the X stage done
+  uint64_t xfull[XS_MAX];   // both halves of the X stage landed (even CTA)
+  uint64_t xempty[XS_MAX];  // pair MMAs reading the X stage done
   uint64_t wfull[WS];   // this CTA's qweight and scale tiles landed
   uint64_t wempty[WS];  // weight tiles read by this CTA's group warps
   uint64_t afull[AS];   // A slot written by the group warps of both CTAs (even CTA)
   uint64_t aempty[AS];  // pair MMAs reading the A slot done
-  uint64_t dfull;       // all MMAs of the current tile done
-  uint64_t dempty;      // accumulator read out by every group warp of both CTAs (even CTA)
+  uint64_t dfull[2];    // all MMAs of the tile done
+  uint64_t dempty[2];   // accumulator read out by both CTAs' read-out warps (even CTA)
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -112,6 +127,7 @@ __device__ __forceinline__ int box_index(int n) { return n <= 64 ? 0 : (n <= 128
 
 // The tiles of one cluster: tile = cluster + i * clusters for i = 0, 1, ...;
 // column pair fastest.
+template <class Table>
 struct Walk {
   int cluster, clusters, n_pairs, tiles;
   Table table;
@@ -130,7 +146,9 @@ struct Walk {
 // (N, or K in the gradient).  scale_rows: scale rows that 128 k touch.
 // x3d: X is read through a [C/64][R][64] view, one copy per stage (C a
 // multiple of 64); otherwise through [R][C], one copy per 64-column half.
-template <bool DX>
+// WPS: consecutive packed words of a column that share one scale (2, 4, 8 or,
+// for groups of 128 and more, 16; not used in the gradient).
+template <bool DX, int BT, int WPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     experts_pair_kernel(const __grid_constant__ XMaps x_maps,
                         const __grid_constant__ CUtensorMap qw_map,
@@ -138,6 +156,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         const __grid_constant__ CUtensorMap y_map, const int32_t* offsets, int R,
                         int C, int O, int E, int group_shift, int scale_rows, int x3d,
                         int n_pairs, uint16_t* y, int* err) {
+  using G_ = Geo<BT>;
+  constexpr int XS = G_::XS, X_STAGE_BYTES = G_::X_STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned base; the same offset in both CTAs, so that one MMA
   // descriptor and one barrier offset name the matching buffers of the pair
@@ -163,8 +183,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&bar->afull[j], 2 * 4);   // the slot's group warps in both CTAs
       mbar_init(&bar->aempty[j], 1);      // one pair commit
     }
-    mbar_init(&bar->dfull, 1);                 // one pair commit per tile
-    mbar_init(&bar->dempty, 2 * DQ_WARPS);     // every group warp of both CTAs
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->dfull[i], 1);       // one pair commit per tile
+      mbar_init(&bar->dempty[i], 2 * 4);  // the read-out warps of both CTAs
+    }
     bar->abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -181,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
   // the offsets and X may come from the previous kernel of the stream
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  Walk walk;
+  Walk<typename G_::Table> walk;
   walk.cluster = (int)(blockIdx.x >> 1);
   walk.clusters = (int)(gridDim.x >> 1);
   walk.n_pairs = n_pairs;
@@ -200,7 +222,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // the even CTA's barriers that both CTAs signal
   const uint32_t xfull_even = map_to_rank(smem_u32(&bar->xfull[0]), 0);
   const uint32_t afull_even = map_to_rank(smem_u32(&bar->afull[0]), 0);
-  const uint32_t dempty_even = map_to_rank(smem_u32(&bar->dempty), 0);
+  const uint32_t dempty_even = map_to_rank(smem_u32(&bar->dempty[0]), 0);
 
   if (warp == 0 || warp == 2) {
     // ---------------- TMA producers: X half (warp 0), weights (warp 2) ----------------
@@ -308,200 +330,164 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ---------------- pair MMA issuer (even CTA) ----------------
     if (even) {
       bool ok = true;
-      int g = 0, it = 0;
+      int it = 0, s = 0, a = 0, last_n = 0;
+      uint32_t xph = 0, aph = 0;
       for (; it < NT && ok; ++it) {
         int o0;
         const int n = walk.at(it, rank, o0).n;
         const uint32_t idesc = idesc_f16_f32(2 * BW, n);
         const uint32_t half_bytes = 4096u << box_index(n);
-        if (it > 0) {
-          // the previous tile's accumulator has been read out by every group
-          // warp of both CTAs
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->dempty, (uint32_t)(it - 1) & 1u,
-                                                         abort_flag, kWaitLimitNs));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        for (int kb = 0; kb < KB; ++kb, ++g) {
-          const int s = g % XS, a = g % AS;
+        const uint32_t d = tmem + D_COL + (n <= (int)D_HALF ? (it & 1) * D_HALF : 0u);
+        // the tile before the last has been read out; the last one too, where
+        // the two share accumulator columns
+        if (it > 1)
           ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar->xfull[s], (uint32_t)(g / XS) & 1u, abort_flag,
-                                            kWaitLimitNs) &&
-                              mbar_wait_bounded(&bar->afull[a], (uint32_t)(g / AS) & 1u,
-                                                abort_flag, kWaitLimitNs));
+                          mbar_wait_bounded(&bar->dempty[it & 1], (uint32_t)((it - 2) >> 1) & 1u,
+                                            abort_flag, kWaitLimitNs));
+        if (ok && it > 0 && max(n, last_n) > (int)D_HALF)
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->dempty[(it - 1) & 1],
+                                                         (uint32_t)((it - 1) >> 1) & 1u,
+                                                         abort_flag, kWaitLimitNs));
+        if (!ok) break;
+        tc_fence_after();
+        last_n = n;
+        for (int kb = 0; kb < KB; ++kb) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                              mbar_wait_bounded(&bar->afull[a], aph, abort_flag,
+                                                kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t b_desc0 = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES));
+          const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES));
+          const uint64_t b_hi = b_lo + (uint64_t)(half_bytes >> 4);
           const uint32_t a_base = tmem + A_COL + a * A_STAGE_COLS;
           const int nk = min(BK, C - kb * BK + 15) / 16;  // k16 steps holding columns below C
+          const uint32_t keep = kb > 0 ? 1u : 0u;
           if (elect_one()) {
+            if (nk == BK / 16) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              if (kk < nk)
-                mma_f16_ts_pair(tmem + D_COL, a_base + kk * 8,
-                                b_desc0 + (uint64_t)(((kk >> 2) * half_bytes +
-                                                      (kk & 3) * 32) >> 4),
-                                idesc, (kb | kk) != 0 ? 1u : 0u);
+              for (int kk = 0; kk < BK / 16; ++kk)
+                mma_f16_ts_pair(d, a_base + kk * 8,
+                                (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
+                                kk > 0 ? 1u : keep);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < nk; ++kk)
+                mma_f16_ts_pair(d, a_base + kk * 8,
+                                (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
+                                kk > 0 ? 1u : keep);
+            }
             mma_commit_pair(&bar->xempty[s], kPairMask);
             mma_commit_pair(&bar->aempty[a], kPairMask);
+            if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
           }
           __syncwarp();
+          if (++s == XS) {
+            s = 0;
+            xph ^= 1u;
+          }
+          if (++a == AS) {
+            a = 0;
+            aph ^= 1u;
+          }
         }
-        if (!ok) break;
-        if (elect_one()) mma_commit_pair(&bar->dfull, kPairMask);  // tile done
-        __syncwarp();
       }
       if (!ok) {
         if (lane == 0) record_timeout(err, bar);
         // wait for the MMAs already issued before anyone frees TMEM
-        if (elect_one()) mma_commit_pair(&bar->dfull, kPairMask);
+        if (elect_one()) mma_commit_pair(&bar->aempty[a], kPairMask);
         __syncwarp();
         int never = 0;
-        mbar_wait_bounded(&bar->dfull, (uint32_t)it & 1u, &never, kDrainLimitNs);
+        mbar_wait_bounded(&bar->aempty[a], aph, &never, kDrainLimitNs);
       }
     }
     __syncwarp();  // the whole warp reaches the cluster barrier below together
-  } else {
-    // ---------------- dequantisation and accumulator read-out ----------------
+  } else if (warp < EPI_WARP0) {
+    // ---------------- dequantisation ----------------
     const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
-    const int grp = (warp - DQ_WARP0) >> 2;  // stages g = grp mod DQ_GROUPS
-    const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
-    const int col = 32 * quarter + lane;     // this thread's TMEM lane: its output column
-    const int j = grp;                       // this group's A slot
-    uint8_t* ystage = smem + Y_OFF + (grp * 4 + quarter) * Y_WARP_BYTES;
-
-    // Reads out tile d's accumulator (this warp's 32 lanes x its group's TPG
-    // tokens), hands it back to the MMA warp, and stores the FP16 values
-    // through this warp's staging block.  False if the wait expired.
-    auto drain = [&](int d) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded<true>(&bar->dfull, (uint32_t)d & 1u,
-                                                           abort_flag, kWaitLimitNs)))
-        return false;
-      int o0;
-      const ExpertTile tt = walk.at(d, rank, o0);
-      const int live = min(TPG, tt.rows - grp * TPG);  // this group's tokens inside the tile
-      tc_fence_after();
-      uint32_t v0[32], v1[32];
-      if (live > 0) {
-        tmem_ld_32x32b_x32(tmem + lane_addr + D_COL + grp * TPG, v0);
-        tmem_ld_32x32b_x32(tmem + lane_addr + D_COL + grp * TPG + 32, v1);
-        tmem_wait_ld();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(dempty_even);  // the MMAs may overwrite it now
-      const int c0 = o0 + 32 * quarter;
-      if (live <= 0 || c0 >= O) return true;
-      if (lane == 0) bulk_wait_read_all();  // the block's previous store has read it
-      __syncwarp();
-      uint16_t* ys = reinterpret_cast<uint16_t*>(ystage);
-#pragma unroll
-      for (int q = 0; q < 32; ++q)
-        ys[q * 32 + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(v0[q])));
-#pragma unroll
-      for (int q = 0; q < 32; ++q)
-        ys[(32 + q) * 32 + lane] = __half_as_ushort(__float2half_rn(__uint_as_float(v1[q])));
-      const int row = tt.row0 + grp * TPG;
-      if (live == TPG) {
-        fence_proxy_async_smem();  // the staging writes are visible to the store
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&y_map, ystage, c0, row);
-          bulk_commit_group();
-        }
-      } else {
-        // the tile ends inside the block: its rows only, 16 bytes at a time
-        __syncwarp();
-        for (int i = lane; i < 4 * live; i += 32) {
-          const int c = c0 + 8 * (i & 3);
-          if (c < O)
-            *reinterpret_cast<uint4*>(y + (int64_t)(row + (i >> 2)) * O + c) =
-                *reinterpret_cast<const uint4*>(ystage + 16 * i);
-        }
-        __syncwarp();
-      }
-      return true;
-    };
-
+    const int j = (warp - DQ_WARP0) >> 2;    // group: stages g = j mod 4, A slot j
+    const uint32_t a_slot =
+        tmem + ((uint32_t)(32 * quarter) << 16) + A_COL + j * A_STAGE_COLS;
     // forward: this thread's column in weight slot 0; gradient: its packed
-    // row, the byte and nibble of its k, and the matching constants
-    const int prow = DX ? col >> 3 : 0;
-    const uint8_t* qw0 = smem + W_OFF + (DX ? prow * QW_ROW_BYTES : col * 4);
-    const uint8_t* sc0 = smem + W_OFF + QW_STAGE_BYTES +
-                         (DX ? (group_shift >= 7 ? 0 : (prow * 8) >> group_shift) * S_ROW_BYTES
-                             : col * 2);
-    const uint32_t byte = (uint32_t)(col & 7) >> 1;
-    const uint32_t pick = byte | byte << 4 | (byte + 4) << 8 | (byte + 4) << 12;
-    const bool high = col & 1;
-    const uint32_t nib = high ? 0x00F000F0u : 0x000F000Fu;
-    const uint32_t unit = high ? kOneSixteenth : 0x3C003C00u;  // half2(1, 1)
-    const uint32_t zero = high ? kMinus72 : 0xE408E408u;       // half2(-1032, -1032)
+    // row, its four columns of every sixteen, and its half of their words
+    const int col = 32 * quarter + lane;
+    const int prow = 4 * quarter + (lane >> 3);
+    const uint8_t* qw0 =
+        smem + W_OFF + (DX ? prow * QW_ROW_BYTES + (lane & 3) * 16 : col * 4);
+    const uint8_t* sc0 =
+        smem + W_OFF + QW_STAGE_BYTES +
+        (DX ? (group_shift >= 7 ? 0 : (prow * 8) >> group_shift) * S_ROW_BYTES + (lane & 3) * 8
+            : col * 2);
+    const uint32_t half = (uint32_t)(lane >> 2) & 1u;  // k 0..3 or 4..7 of the words
+    const uint32_t pick_lo = half ? 0x6622u : 0x4400u;  // first byte of two words' halves
+    const uint32_t pick_hi = half ? 0x7733u : 0x5511u;  // second byte
 
     bool ok = true;
-    int drained = 0;  // tiles whose accumulator this warp has read out
-    for (int g = grp; g < G; g += DQ_GROUPS) {
-      // Read out every finished tile before this stage.  One must be read
-      // out first if this stage's A slot was last used by a later tile, whose
-      // MMAs wait for the accumulator.
-      const int it = g / KB;
-      while (drained < it) {
-        const bool forced = g - AS >= (drained + 1) * KB;
-        const bool done = __shfl_sync(
-            0xffffffffu, (int)mbar_test_wait(smem_u32(&bar->dfull), (uint32_t)drained & 1u), 0);
-        if (!forced && !done) break;
-        ok = drain(drained);
-        if (!ok) break;
-        ++drained;
-      }
-      if (!ok) {
-        if (lane == 0) record_timeout(err, bar);
-        break;
-      }
-      const uint32_t ph = (uint32_t)(g / DQ_GROUPS) & 1u;  // A slot phase
-      const int jw = g % WS;                                // weight slot
-      const uint32_t pw = (uint32_t)(g / WS) & 1u;
+    int jw = j;                  // weight slot and its phase
+    uint32_t pw = 0, ph = 0;     // ... and the A slot's
+    for (int g = j; g < G; g += DQ_GROUPS) {
       const uint8_t* qw = qw0 + jw * W_STAGE_BYTES;
       const uint8_t* sc = sc0 + jw * W_STAGE_BYTES;
       // qweight and scale tiles of the stage have landed
       ok = __all_sync(0xffffffffu,
                       mbar_wait_bounded<true>(&bar->wfull[jw], pw, abort_flag, kWaitLimitNs));
-      if (!ok) {
-        if (lane == 0) record_timeout(err, bar);
-        break;
+      if (!ok) break;
+      bool small = false;  // one form for the whole stage, so that its branch is the warp's
+      if constexpr (!DX) {
+        small = true;
+#pragma unroll
+        for (int r = 0; r < BK / 8; r += WPS)
+          small = small && scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
+                               sc + r / WPS * S_ROW_BYTES));
+        small = __all_sync(0xffffffffu, small);
       }
       // the stage's 128 k (or n), one half (32 TMEM columns) at a time
-      uint32_t cells[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        uint32_t cells[32];
         if constexpr (DX) {
+          // cells 0..15: k 0 and 1 of the thread's half words, 16..31: k 2 and 3
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // eight columns n: two words' quads, one of scales
-            const uint4 wa = *reinterpret_cast<const uint4*>(qw + (64 * h + 8 * i) * 4);
-            const uint4 wb = *reinterpret_cast<const uint4*>(qw + (64 * h + 8 * i + 4) * 4);
-            const uint4 s8 = *reinterpret_cast<const uint4*>(sc + (64 * h + 8 * i) * 2);
-            const uint32_t w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-            const uint32_t s2[4] = {s8.x, s8.y, s8.z, s8.w};
+          for (int i = 0; i < 4; ++i) {  // sixteen columns n, four of them this thread's
+            const uint4 w = *reinterpret_cast<const uint4*>(qw + (64 * h + 16 * i) * 4);
+            const uint2 s4 = *reinterpret_cast<const uint2*>(sc + (64 * h + 16 * i) * 2);
+            const uint32_t lo[2] = {prmt(w.x, w.y, pick_lo), prmt(w.z, w.w, pick_lo)};
+            const uint32_t hi[2] = {prmt(w.x, w.y, pick_hi), prmt(w.z, w.w, pick_hi)};
+            const uint32_t s2[2] = {s4.x, s4.y};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t t = prmt(w[2 * q], w[2 * q + 1], pick);
-              // 1024 + q, or 1024 + 16 q; then q - 8 exactly; then one rounding
-              const uint32_t c = hfma2_rn(lop3_and_or(t, nib, kMagic1024), unit, zero);
-              cells[4 * i + q] = hmul2_rn(c, s2[q]);
+            for (int q = 0; q < 2; ++q) {  // column pairs: q - 8 exactly, then one rounding
+              cells[4 * i + q] = hmul2_rn(
+                  hsub2_rn(lop3_and_or(lo[q], 0x000F000Fu, kMagic1024), kMinus1032), s2[q]);
+              cells[4 * i + 2 + q] =
+                  hmul2_rn(hfma2_rn(lop3_and_or(lo[q], 0x00F000F0u, kMagic1024), kOneSixteenth,
+                                    kMinus72), s2[q]);
+              cells[16 + 4 * i + q] = hmul2_rn(
+                  hsub2_rn(lop3_and_or(hi[q], 0x000F000Fu, kMagic1024), kMinus1032), s2[q]);
+              cells[16 + 4 * i + 2 + q] =
+                  hmul2_rn(hfma2_rn(lop3_and_or(hi[q], 0x00F000F0u, kMagic1024), kOneSixteenth,
+                                    kMinus72), s2[q]);
             }
           }
         } else {
+          uint32_t w[8];
 #pragma unroll
-          for (int r8 = 0; r8 < 8; ++r8) {
-            const int r = 8 * h + r8;
-            // scale row of packed row r inside the stage (0 unless the group is
-            // smaller than the 128-k stage)
-            const int gl = group_shift >= 7 ? 0 : (r * 8) >> group_shift;
-            const uint16_t sv = *reinterpret_cast<const uint16_t*>(sc + gl * S_ROW_BYTES);
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(qw + r * QW_ROW_BYTES);
-            uint32_t nat[4];
-            dequant_word_natural(w, half2_broadcast(sv), nat);
+          for (int r = 0; r < 8; ++r)
+            w[r] = *reinterpret_cast<const uint32_t*>(qw + (8 * h + r) * QW_ROW_BYTES);
+          constexpr int PER = WPS < 8 ? WPS : 8;  // words of this half that share a scale
 #pragma unroll
-            for (int q = 0; q < 4; ++q) cells[4 * r8 + q] = nat[q];
+          for (int r0 = 0; r0 < 8; r0 += PER) {
+            const uint32_t s2 = half2_broadcast(*reinterpret_cast<const uint16_t*>(
+                sc + (8 * h + r0) / WPS * S_ROW_BYTES));
+            if (small) {
+              uint32_t b2, c2;
+              subnormal_form_constants(s2, b2, c2);
+#pragma unroll
+              for (int r = r0; r < r0 + PER; ++r)
+                dequant_word_natural_small_scale(w[r], b2, c2, cells + 4 * r);
+            } else {
+#pragma unroll
+              for (int r = r0; r < r0 + PER; ++r) dequant_word_natural(w[r], s2, cells + 4 * r);
+            }
           }
         }
         if (h == 0) {
@@ -514,22 +500,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->wempty[jw]);  // weight tiles of the stage read
         }
-        tmem_st_32x32b_x32(tmem + lane_addr + A_COL + j * A_STAGE_COLS + 32 * h, cells);
+        if constexpr (DX) {
+          tmem_st_16x256b_x4(a_slot + 32 * h, cells);
+          tmem_st_16x256b_x4(a_slot + (16u << 16) + 32 * h, cells + 16);
+        } else {
+          tmem_st_32x32b_x32(a_slot + 32 * h, cells);
+        }
       }
-      if (!ok) {
-        if (lane == 0) record_timeout(err, bar);
-        break;
-      }
+      if (!ok) break;
       tmem_wait_st();  // the whole warp's cells are in TMEM
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(afull_even + 8u * (uint32_t)j);
+      ph ^= 1u;
+      jw += DQ_GROUPS;
+      if (jw >= WS) {
+        jw -= WS;
+        pw ^= 1u;
+      }
     }
-    // the tiles not read out yet
-    while (ok && drained < NT) {
-      ok = drain(drained);
-      if (!ok && lane == 0) record_timeout(err, bar);
-      ++drained;
+    if (!ok && lane == 0) record_timeout(err, bar);
+    __syncwarp();
+  } else {
+    // ---------------- accumulator read-out ----------------
+    const int quarter = warp & 3;
+    const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
+    uint8_t* ystage = smem + Y_OFF + (warp - EPI_WARP0) * Y_BLOCKS * Y_BLOCK_BYTES;
+    // the output column (of the warp's 32) that this TMEM lane holds
+    const int ycol = DX ? 4 * (lane & 7) + (lane >> 3) : lane;
+    int blk = 0;
+    for (int it = 0; it < NT; ++it) {
+      int o0;
+      const ExpertTile tt = walk.at(it, rank, o0);
+      const int c0 = o0 + 32 * quarter;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_bounded<true>(&bar->dfull[it & 1], (uint32_t)(it >> 1) & 1u,
+                                              abort_flag, kWaitLimitNs))) {
+        if (lane == 0) record_timeout(err, bar);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem + lane_addr + D_COL + (tt.n <= (int)D_HALF ? (it & 1) * D_HALF : 0u);
+      const int blocks = c0 < O ? (tt.rows + Y_ROWS - 1) / Y_ROWS : 0;
+#pragma unroll 1
+      for (int b = 0; b < blocks; ++b) {
+        uint32_t v[Y_ROWS];
+        tmem_ld_32x32b_x32(d + Y_ROWS * b, v);
+        // the store that used this block last has read it: all but the latest
+        if (lane == 0) bulk_wait_read_but_one();
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && b == blocks - 1)  // all read: the MMAs may overwrite it
+          mbar_arrive_cluster(dempty_even + 8u * (uint32_t)(it & 1));
+        uint8_t* yb = ystage + blk * Y_BLOCK_BYTES;
+        blk ^= 1;
+        uint16_t* ys = reinterpret_cast<uint16_t*>(yb) + ycol;
+#pragma unroll
+        for (int q = 0; q < Y_ROWS; ++q)
+          ys[q * 32] = __half_as_ushort(__float2half_rn(__uint_as_float(v[q])));
+        const int row = tt.row0 + Y_ROWS * b, live = min(Y_ROWS, tt.rows - Y_ROWS * b);
+        if (live == Y_ROWS) {
+          fence_proxy_async_smem();  // the staging writes are visible to the store
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&y_map, yb, c0, row);
+            bulk_commit_group();
+          }
+        } else {
+          // the tile ends inside the block: its rows only, 16 bytes at a time
+          __syncwarp();
+          for (int i = lane; i < 4 * live; i += 32) {
+            const int c = c0 + 8 * (i & 3);
+            if (c < O)
+              *reinterpret_cast<uint4*>(y + (int64_t)(row + (i >> 2)) * O + c) =
+                  *reinterpret_cast<const uint4*>(yb + 16 * i);
+          }
+          // (an empty group keeps the count of groups and blocks in step)
+          if (lane == 0) bulk_commit_group();
+          __syncwarp();
+        }
+      }
+      if (blocks == 0) {  // none of the warp's columns exist
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(dempty_even + 8u * (uint32_t)(it & 1));
+      }
     }
     if (lane == 0) bulk_wait_all();  // this warp's stores have completed
     __syncwarp();
@@ -546,8 +602,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-template <bool DX>
-cudaError_t launch_pair(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+template <bool DX, int BT, int WPS>
+cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
                         const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
                         int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
   const int64_t C = DX ? N : K, O = DX ? K : N;
@@ -581,17 +637,17 @@ cudaError_t launch_pair(const uint16_t* x, const int32_t* qweight, const uint16_
                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_map_3d(&s_map, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, sdims, sstrides, sbox,
                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      // Y blocks of 32 columns x 64 tokens, one per dequantisation warp
+      // Y blocks of 32 columns x 32 tokens
       !encode_map_2d(&y_map, y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)O, (uint64_t)R,
-                     (uint64_t)O * 2, 32, TPG, CU_TENSOR_MAP_SWIZZLE_NONE))
+                     (uint64_t)O * 2, 32, Y_ROWS, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   static std::once_flag attr_once[64];
   static cudaError_t attr_err[64];
   const int d = dev.device & 63;
   std::call_once(attr_once[d], [&] {
-    attr_err[d] = cudaFuncSetAttribute(experts_pair_kernel<DX>,
+    attr_err[d] = cudaFuncSetAttribute(experts_pair_kernel<DX, BT, WPS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       1024 + TABLE_OFF + Table::bytes(GPTQ_MOE_MAX_EXPERTS));
+                                       1024 + TABLE_OFF + Geo<BT>::Table::bytes(GPTQ_MOE_MAX_EXPERTS));
   });
   if (attr_err[d] != cudaSuccess) return attr_err[d];
   // column pairs of 2 x 128 (with an odd count of 128-column tiles the last
@@ -604,16 +660,25 @@ cudaError_t launch_pair(const uint16_t* x, const int32_t* qweight, const uint16_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = 1024 + TABLE_OFF + Table::bytes((int)E);
+  cfg.dynamicSmemBytes = 1024 + TABLE_OFF + Geo<BT>::Table::bytes((int)E);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, experts_pair_kernel<DX>, x_maps, qw_map, s_map, y_map, offsets,
+  return cudaLaunchKernelEx(&cfg, experts_pair_kernel<DX, BT, WPS>, x_maps, qw_map, s_map, y_map, offsets,
                             (int)R, (int)C, (int)O, (int)E, group_shift, scale_rows, x3d,
                             (int)n_pairs, y, dev.error_word);
+}
+
+// The token tile, from the rows an expert has on average.
+template <bool DX, int WPS>
+cudaError_t launch_pair(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
+                        const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
+                        int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
+  const auto launch = R <= 128 * E ? launch_bt<DX, 128, WPS> : launch_bt<DX, 256, WPS>;
+  return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
 }
 
 }  // namespace
@@ -622,15 +687,19 @@ cudaError_t launch_experts_pair(const uint16_t* x, const int32_t* qweight, const
                                 const int32_t* offsets, uint16_t* y, int64_t R, int64_t K,
                                 int64_t N, int64_t E, int group_shift, cudaStream_t stream,
                                 const DeviceInfo& dev) {
-  return launch_pair<false>(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
+  const auto launch = group_shift == 4   ? launch_pair<false, 2>
+                      : group_shift == 5 ? launch_pair<false, 4>
+                      : group_shift == 6 ? launch_pair<false, 8>
+                                         : launch_pair<false, 16>;
+  return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
 }
 
 cudaError_t launch_experts_dx(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales,
                               const int32_t* offsets, uint16_t* dx, int64_t R, int64_t K,
                               int64_t N, int64_t E, int group_shift, cudaStream_t stream,
                               const DeviceInfo& dev) {
-  return launch_pair<true>(dy, qweight, scales, offsets, dx, R, K, N, E, group_shift, stream,
-                           dev);
+  return launch_pair<true, 16>(dy, qweight, scales, offsets, dx, R, K, N, E, group_shift, stream,
+                               dev);
 }
 
 }  // namespace gptq
