@@ -332,6 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       int it = 0, s = 0, a = 0, last_n = 0;
       uint32_t xph = 0, aph = 0;
+      bool ready = false;  // the next stage's operands were seen to be there
       for (; it < NT && ok; ++it) {
         int o0;
         const int n = walk.at(it, rank, o0).n;
@@ -352,12 +353,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_after();
         last_n = n;
         for (int kb = 0; kb < KB; ++kb) {
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
-                              mbar_wait_bounded(&bar->afull[a], aph, abort_flag,
-                                                kWaitLimitNs));
+          if (!ready)
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                                mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
+          // Is the next stage there already?  Asked before this stage's MMAs are
+          // issued and answered after: a wait that has nothing to wait for still
+          // costs 200 cycles here, two of them half of a small tile's stage.
+          const int s1 = s + 1 < XS ? s + 1 : 0, a1 = a + 1 < AS ? a + 1 : 0;
+          const uint32_t xph1 = s1 ? xph : xph ^ 1u, aph1 = a1 ? aph : aph ^ 1u;
+          const bool x1 = mbar_test_wait(smem_u32(&bar->xfull[s1]), xph1);
+          const bool w1 = mbar_test_wait(smem_u32(&bar->afull[a1]), aph1);
           const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES));
           const uint64_t b_hi = b_lo + (uint64_t)(half_bytes >> 4);
           const uint32_t a_base = tmem + A_COL + a * A_STAGE_COLS;
@@ -382,14 +390,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
           }
           __syncwarp();
-          if (++s == XS) {
-            s = 0;
-            xph ^= 1u;
-          }
-          if (++a == AS) {
-            a = 0;
-            aph ^= 1u;
-          }
+          ready = __all_sync(0xffffffffu, x1 && w1);
+          s = s1;
+          a = a1;
+          xph = xph1;
+          aph = aph1;
         }
       }
       if (!ok) {
