@@ -32,9 +32,13 @@
 // one byte permute collects a byte of two columns' words, whose two nibbles
 // are two k of that column pair.  Stored in the 16-lane, 256-bit form of
 // tcgen05.st, a thread's four k lie in TMEM lanes r, r + 8, r + 16 and r + 24
-// of its quarter: lane l holds k = 4 (l mod 8) + l / 8, which the read-out
-// undoes.  (With a lane per thread, every word was read by eight threads and
-// shared memory bound the kernel.)
+// of its quarter.  (With a lane per thread, every word was read by eight
+// threads and shared memory bound the kernel.)
+//
+// So TMEM lane l of a quarter holds output column 4 (l mod 8) + l / 8 (the
+// forward dequantisation reads its words accordingly), and the 16-lane form of
+// tcgen05.ld hands a thread four neighbouring columns of a token: the read-out
+// packs and stores them eight bytes at a time.
 //
 // Every wait is bounded in time; on expiry the CTA records GPTQ_ERR_TIMEOUT
 // in the device error word and winds down.  Both CTAs always reach the final
@@ -79,7 +83,8 @@ constexpr int Y_BLOCKS = 2;                        // per read-out warp, in turn
 constexpr int W_OFF = X_RING_BYTES;
 constexpr int Y_OFF = W_OFF + WS * W_STAGE_BYTES;
 constexpr int BAR_OFF = Y_OFF + 4 * Y_BLOCKS * Y_BLOCK_BYTES;
-constexpr int TABLE_OFF = BAR_OFF + 512;
+constexpr int LIST_OFF = BAR_OFF + 512;
+constexpr int TABLE_OFF = LIST_OFF + 256 * 16;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t D_COL = 0;              // accumulators: columns [0, 256)
 constexpr uint32_t D_HALF = 128;           // ... tiles of up to 128 rows alternate
@@ -126,19 +131,50 @@ struct XMaps {
 __device__ __forceinline__ int box_index(int n) { return n <= 64 ? 0 : (n <= 128 ? 1 : 2); }
 
 // The tiles of one cluster: tile = cluster + i * clusters for i = 0, 1, ...;
-// column pair fastest.
+// column pair fastest.  The first LISTED are looked up once, all threads at a
+// time, and kept in shared memory: a search of the table takes over 500 cycles,
+// in the MMA warp as long as two of a small tile's stages.
+constexpr int LISTED = (TABLE_OFF - LIST_OFF) / 16;
+struct ListedTile {
+  int e, row0, rows_n, o0;  // rows | n << 16; first column of the pair
+};
+static_assert(sizeof(ListedTile) == 16, "one 16-byte load");
+
 template <class Table>
 struct Walk {
   int cluster, clusters, n_pairs, tiles;
   Table table;
+  ListedTile* list;
   __device__ int count() const {
     return cluster < tiles ? (tiles - cluster + clusters - 1) / clusters : 0;
   }
+  __device__ ExpertTile find(int i, int& o0) const {
+    const int tile = cluster + i * clusters;
+    o0 = 2 * (tile % n_pairs) * BW;
+    return table.find(tile / n_pairs);
+  }
+  // Called by every thread of the CTA (`threads` of them); a barrier must
+  // follow.
+  __device__ void fill(int threads) {
+    const int n = min(count(), LISTED);
+    for (int i = threadIdx.x; i < n; i += threads) {
+      int o0;
+      const ExpertTile t = find(i, o0);
+      list[i] = ListedTile{t.e, t.row0, t.rows | t.n << 16, o0};
+    }
+  }
   // This CTA's first output column in tile i, and the token tile.
   __device__ ExpertTile at(int i, uint32_t rank, int& o0) const {
-    const int tile = cluster + i * clusters;
-    o0 = (2 * (tile % n_pairs) + (int)rank) * BW;
-    return table.find(tile / n_pairs);
+    ExpertTile t;
+    if (i < LISTED) {
+      const int4 v = *reinterpret_cast<const int4*>(list + i);
+      t = ExpertTile{v.x, v.y, v.z & 0xFFFF, v.z >> 16};
+      o0 = v.w;
+    } else {
+      t = find(i, o0);
+    }
+    o0 += (int)rank * BW;
+    return t;
   }
 };
 
@@ -210,11 +246,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   walk.table.place(smem + TABLE_OFF, E);
   walk.table.build(offsets, R, THREADS, err);
   walk.tiles = walk.table.tiles() * n_pairs;
+  walk.list = reinterpret_cast<ListedTile*>(smem + LIST_OFF);
+  walk.fill(THREADS);
   const int NT = walk.count();          // tiles of this cluster
   const int KB = (C + BK - 1) / BK;     // stages per tile
   const int G = NT * KB;                // stages of this cluster, over all its tiles
-  // both CTAs' barriers are initialised and TMEM is allocated before any
-  // thread signals the other CTA
+  // the list is complete; both CTAs' barriers are initialised and TMEM is
+  // allocated before any thread signals the other CTA
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -352,26 +390,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         last_n = n;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!ready)
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
-                                mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs));
-          if (!ok) break;
-          tc_fence_after();
-          // Is the next stage there already?  Asked before this stage's MMAs are
-          // issued and answered after: a wait that has nothing to wait for still
-          // costs 200 cycles here, two of them half of a small tile's stage.
+        // With small tiles two stages at a time where there are two: the warp's
+        // own waits and commits cost as much as a small tile's MMAs.  (With 256
+        // tokens waiting for two of the three X stages costs more than it saves.)
+        constexpr int TURN = BT <= 128 ? 2 : 1;
+        for (int kb = 0; kb < KB; kb += TURN) {
+          const bool two = TURN == 2 && kb + 1 < KB;
           const int s1 = s + 1 < XS ? s + 1 : 0, a1 = a + 1 < AS ? a + 1 : 0;
           const uint32_t xph1 = s1 ? xph : xph ^ 1u, aph1 = a1 ? aph : aph ^ 1u;
-          const bool x1 = mbar_test_wait(smem_u32(&bar->xfull[s1]), xph1);
-          const bool w1 = mbar_test_wait(smem_u32(&bar->afull[a1]), aph1);
-          const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES));
-          const uint64_t b_hi = b_lo + (uint64_t)(half_bytes >> 4);
-          const uint32_t a_base = tmem + A_COL + a * A_STAGE_COLS;
-          const int nk = min(BK, C - kb * BK + 15) / 16;  // k16 steps holding columns below C
-          const uint32_t keep = kb > 0 ? 1u : 0u;
-          if (elect_one()) {
+          if (!ready)
+            ok = __all_sync(
+                0xffffffffu,
+                mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                    mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
+                    (!two ||
+                     (mbar_wait_bounded(&bar->xfull[s1], xph1, abort_flag, kWaitLimitNs) &&
+                      mbar_wait_bounded(&bar->afull[a1], aph1, abort_flag, kWaitLimitNs))));
+          if (!ok) break;
+          tc_fence_after();
+          // Are the next two there already?  Asked before these MMAs are issued
+          // and answered after: a wait that has nothing to wait for still costs
+          // 200 cycles here.
+          int s2 = s1, a2 = a1;
+          uint32_t xph2 = xph1, aph2 = aph1;
+          if (two) {
+            s2 = s1 + 1 < XS ? s1 + 1 : 0;
+            a2 = a1 + 1 < AS ? a1 + 1 : 0;
+            xph2 = s2 ? xph1 : xph1 ^ 1u;
+            aph2 = a2 ? aph1 : aph1 ^ 1u;
+          }
+          bool next = mbar_test_wait(smem_u32(&bar->xfull[s2]), xph2) &
+                      mbar_test_wait(smem_u32(&bar->afull[a2]), aph2);
+          if (TURN == 2) {
+            const int s3 = s2 + 1 < XS ? s2 + 1 : 0, a3 = a2 + 1 < AS ? a2 + 1 : 0;
+            next &= mbar_test_wait(smem_u32(&bar->xfull[s3]), s3 ? xph2 : xph2 ^ 1u) &
+                    mbar_test_wait(smem_u32(&bar->afull[a3]), a3 ? aph2 : aph2 ^ 1u);
+          }
+          // the stage's MMAs; k16 steps that hold columns below C
+          const auto issue = [&](int sx, int ax, int kbx) {
+            const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + sx * X_STAGE_BYTES));
+            const uint64_t b_hi = b_lo + (uint64_t)(half_bytes >> 4);
+            const uint32_t a_base = tmem + A_COL + ax * A_STAGE_COLS;
+            const int nk = min(BK, C - kbx * BK + 15) / 16;
+            const uint32_t keep = kbx > 0 ? 1u : 0u;
             if (nk == BK / 16) {
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)
@@ -385,16 +446,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
                                 kk > 0 ? 1u : keep);
             }
-            mma_commit_pair(&bar->xempty[s], kPairMask);
-            mma_commit_pair(&bar->aempty[a], kPairMask);
-            if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
+            mma_commit_pair(&bar->xempty[sx], kPairMask);
+            mma_commit_pair(&bar->aempty[ax], kPairMask);
+          };
+          if (elect_one()) {
+            issue(s, a, kb);
+            if (two) issue(s1, a1, kb + 1);
+            if (kb + TURN >= KB) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
           }
           __syncwarp();
-          ready = __all_sync(0xffffffffu, x1 && w1);
-          s = s1;
-          a = a1;
-          xph = xph1;
-          aph = aph1;
+          ready = __all_sync(0xffffffffu, next);
+          s = s2;
+          a = a2;
+          xph = xph2;
+          aph = aph2;
         }
       }
       if (!ok) {
@@ -415,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tmem + ((uint32_t)(32 * quarter) << 16) + A_COL + j * A_STAGE_COLS;
     // forward: this thread's column in weight slot 0; gradient: its packed
     // row, its four columns of every sixteen, and its half of their words
-    const int col = 32 * quarter + lane;
+    const int col = 32 * quarter + 4 * (lane & 7) + (lane >> 3);
     const int prow = 4 * quarter + (lane >> 3);
     const uint8_t* qw0 =
         smem + W_OFF + (DX ? prow * QW_ROW_BYTES + (lane & 3) * 16 : col * 4);
@@ -531,8 +596,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int quarter = warp & 3;
     const uint32_t lane_addr = (uint32_t)(32 * quarter) << 16;
     uint8_t* ystage = smem + Y_OFF + (warp - EPI_WARP0) * Y_BLOCKS * Y_BLOCK_BYTES;
-    // the output column (of the warp's 32) that this TMEM lane holds
-    const int ycol = DX ? 4 * (lane & 7) + (lane >> 3) : lane;
+    // of every eight tokens this thread reads 2 (lane mod 4) and the next, four
+    // columns each; the block's 64-byte rows have the 64-byte swizzle
+    const int tok0 = 2 * (lane & 3);
+    const uint32_t ybyte = (uint32_t)(lane & 4) << 1;  // which half of a 16-byte chunk
+    const uint32_t ychunk = (uint32_t)lane >> 3;
     int blk = 0;
     for (int it = 0; it < NT; ++it) {
       int o0;
@@ -549,8 +617,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int blocks = c0 < O ? (tt.rows + Y_ROWS - 1) / Y_ROWS : 0;
 #pragma unroll 1
       for (int b = 0; b < blocks; ++b) {
-        uint32_t v[Y_ROWS];
-        tmem_ld_32x32b_x32(d + Y_ROWS * b, v);
+        uint32_t va[16], vb[16];  // the thread's columns 0 and 1, 2 and 3
+        tmem_ld_16x256b_x4(d + Y_ROWS * b, va);
+        tmem_ld_16x256b_x4(d + (16u << 16) + Y_ROWS * b, vb);
         // the store that used this block last has read it: all but the latest
         if (lane == 0) bulk_wait_read_but_one();
         tmem_wait_ld();
@@ -560,10 +629,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mbar_arrive_cluster(dempty_even + 8u * (uint32_t)(it & 1));
         uint8_t* yb = ystage + blk * Y_BLOCK_BYTES;
         blk ^= 1;
-        uint16_t* ys = reinterpret_cast<uint16_t*>(yb) + ycol;
 #pragma unroll
-        for (int q = 0; q < Y_ROWS; ++q)
-          ys[q * 32] = __half_as_ushort(__float2half_rn(__uint_as_float(v[q])));
+        for (int g = 0; g < Y_ROWS / 8; ++g) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int tok = 8 * g + tok0 + t;
+            const __half2 lo = __floats2half2_rn(__uint_as_float(va[4 * g + t]),
+                                                 __uint_as_float(va[4 * g + 2 + t]));
+            const __half2 hi = __floats2half2_rn(__uint_as_float(vb[4 * g + t]),
+                                                 __uint_as_float(vb[4 * g + 2 + t]));
+            *reinterpret_cast<uint2*>(yb + tok * 64 + ((ychunk ^ ((tok >> 1) & 3)) << 4) + ybyte) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                           *reinterpret_cast<const uint32_t*>(&hi));
+          }
+        }
         const int row = tt.row0 + Y_ROWS * b, live = min(Y_ROWS, tt.rows - Y_ROWS * b);
         if (live == Y_ROWS) {
           fence_proxy_async_smem();  // the staging writes are visible to the store
@@ -579,7 +658,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int c = c0 + 8 * (i & 3);
             if (c < O)
               *reinterpret_cast<uint4*>(y + (int64_t)(row + (i >> 2)) * O + c) =
-                  *reinterpret_cast<const uint4*>(yb + 16 * i);
+                  *reinterpret_cast<const uint4*>(yb + (i >> 2) * 64 +
+                                                  (((i & 3) ^ ((i >> 3) & 3)) << 4));
           }
           // (an empty group keeps the count of groups and blocks in step)
           if (lane == 0) bulk_commit_group();
@@ -644,7 +724,7 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
       // Y blocks of 32 columns x 32 tokens
       !encode_map_2d(&y_map, y, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)O, (uint64_t)R,
-                     (uint64_t)O * 2, 32, Y_ROWS, CU_TENSOR_MAP_SWIZZLE_NONE))
+                     (uint64_t)O * 2, 32, Y_ROWS, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   static std::once_flag attr_once[64];
   static cudaError_t attr_err[64];
