@@ -62,26 +62,23 @@ namespace gptq {
 namespace {
 
 constexpr int BW = 128;   // output columns per CTA (TMEM lanes); 256 per pair (MMA M)
-constexpr int BK = 128;   // contraction per pipeline stage (eight k16 MMAs)
-constexpr int XS_MAX = 6;  // X ring stages, at most
-constexpr int WS = 8;     // weight-tile ring stages (qweight + scales)
+constexpr int BK = 128;   // contraction per A slot (eight k16 MMAs)
+constexpr int XS = 3;     // X ring stages
+constexpr int WS_MAX = 8;  // weight-tile ring stages (qweight + scales), at most
 constexpr int AS = 4;     // A slots in TMEM (BK each)
-constexpr int DQ_GROUPS = 4;             // dequantisation groups: group g takes stages g mod 4
+constexpr int DQ_GROUPS = 4;             // dequantisation groups: group g takes slots' worth g mod 4
 constexpr int DQ_WARPS = 4 * DQ_GROUPS;  // one warp per TMEM lane quarter in each group
 constexpr int DQ_WARP0 = 3;  // warps 0, 1, 2: X producer, MMA issuer, weight producer
 constexpr int EPI_WARP0 = DQ_WARP0 + DQ_WARPS;  // four read-out warps
 constexpr int THREADS = (EPI_WARP0 + 4) * 32;
-constexpr int QW_STAGE_BYTES = BW * (BK / 8) * 4;  // 16 packed rows x 128 columns: 8 KB
-constexpr int QW_ROW_BYTES = BW * 4;
-constexpr int S_ROW_BYTES = BW * 2;                // one scale row of the tile: 256 B
-constexpr int S_STAGE_MAX_ROWS = BK / 16;          // group 16: eight rows per stage
-constexpr int W_STAGE_BYTES = QW_STAGE_BYTES + S_STAGE_MAX_ROWS * S_ROW_BYTES;
-constexpr int X_RING_BYTES = 96 * 1024;            // three stages of 256 tokens, six of 128
+constexpr int S_ROW_BYTES = BW * 2;                // a scale row of 128 columns: 256 B
+constexpr int X_STAGE_BYTES = 32 * 1024;           // 128 rows x 128 or 64 rows x 256 columns
+constexpr int W_RING_BYTES = 80 * 1024;
 constexpr int Y_ROWS = 32;                         // tokens per store block
 constexpr int Y_BLOCK_BYTES = Y_ROWS * 32 * 2;     // ... of a read-out warp's 32 columns
 constexpr int Y_BLOCKS = 2;                        // per read-out warp, in turn
-constexpr int W_OFF = X_RING_BYTES;
-constexpr int Y_OFF = W_OFF + WS * W_STAGE_BYTES;
+constexpr int W_OFF = XS * X_STAGE_BYTES;
+constexpr int Y_OFF = W_OFF + W_RING_BYTES;
 constexpr int BAR_OFF = Y_OFF + 4 * Y_BLOCKS * Y_BLOCK_BYTES;
 constexpr int LIST_OFF = BAR_OFF + 512;
 constexpr int TABLE_OFF = LIST_OFF + 256 * 16;
@@ -94,15 +91,23 @@ constexpr uint16_t kPairMask = 0x3;        // both CTAs of the cluster
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 static_assert(A_COL + AS * A_STAGE_COLS <= TMEM_COLS, "TMEM budget");
-static_assert(AS == DQ_GROUPS && WS % DQ_GROUPS == 0,
-              "stage g uses A slot g mod 4 and weight slot g mod WS, both of group g mod 4");
+static_assert(AS == DQ_GROUPS, "A slot j is written by group j");
 
+// A ring stage holds KST of the contraction: 128 with tiles of 256 tokens, 256
+// (two A slots' worth) with smaller ones, whose MMAs are so short that the
+// producers' and the MMA warp's work per stage sets the pace.
 template <int BT>
 struct Geo {
   using Table = ExpertTable<BT, 32>;
-  static constexpr int X_STAGE_BYTES = BT * 128;  // two 64-column halves of BT / 2 rows
-  static constexpr int XS = X_RING_BYTES / X_STAGE_BYTES;
-  static_assert(XS <= XS_MAX, "X ring stages");
+  static constexpr int KST = BT <= 128 ? 256 : 128;
+  static constexpr int H = KST / BK;                 // A slots per stage
+  static constexpr int ATOMS = KST / 64;             // 64-column atoms of X per stage
+  static constexpr int QW_BYTES = BW * (KST / 8) * 4;
+  // scale rows of 16 k each at most (group 16)
+  static constexpr int W_STAGE_BYTES = QW_BYTES + KST / 16 * S_ROW_BYTES;
+  static constexpr int WS = W_RING_BYTES / W_STAGE_BYTES;
+  static_assert(BT / 2 * KST * 2 == X_STAGE_BYTES, "an X stage");
+  static_assert(WS == 8 / H && WS <= WS_MAX, "weight stage f / H mod WS comes round to group j");
 };
 static_assert(1024 + TABLE_OFF + ExpertTable<256, 32>::bytes(GPTQ_MOE_MAX_EXPERTS) <= 227 * 1024,
               "shared memory per CTA");
@@ -110,10 +115,10 @@ static_assert(1024 + TABLE_OFF + ExpertTable<256, 32>::bytes(GPTQ_MOE_MAX_EXPERT
 // Both CTAs hold the full set; xfull, afull and dempty are only used in the
 // even CTA.  dfull and dempty of tile i: entry i mod 2.
 struct PairBarriers {
-  uint64_t xfull[XS_MAX];   // both halves of the X stage landed (even CTA)
-  uint64_t xempty[XS_MAX];  // pair MMAs reading the X stage done
-  uint64_t wfull[WS];   // this CTA's qweight and scale tiles landed
-  uint64_t wempty[WS];  // weight tiles read by this CTA's group warps
+  uint64_t xfull[XS];   // both halves of the X stage landed (even CTA)
+  uint64_t xempty[XS];  // pair MMAs reading the X stage done
+  uint64_t wfull[WS_MAX];   // this CTA's qweight and scale tiles landed
+  uint64_t wempty[WS_MAX];  // weight tiles read by this CTA's group warps
   uint64_t afull[AS];   // A slot written by the group warps of both CTAs (even CTA)
   uint64_t aempty[AS];  // pair MMAs reading the A slot done
   uint64_t dfull[2];    // all MMAs of the tile done
@@ -179,9 +184,9 @@ struct Walk {
 };
 
 // C: the contraction length (K, or N in the gradient); O: the output width
-// (N, or K in the gradient).  scale_rows: scale rows that 128 k touch.
+// (N, or K in the gradient).  scale_bytes: scales of a stage.
 // x3d: X is read through a [C/64][R][64] view, one copy per stage (C a
-// multiple of 64); otherwise through [R][C], one copy per 64-column half.
+// multiple of 64); otherwise through [R][C], one copy per 64-column atom.
 // WPS: consecutive packed words of a column that share one scale (2, 4, 8 or,
 // for groups of 128 and more, 16; not used in the gradient).
 template <bool DX, int BT, int WPS>
@@ -190,10 +195,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         const __grid_constant__ CUtensorMap qw_map,
                         const __grid_constant__ CUtensorMap s_map,
                         const __grid_constant__ CUtensorMap y_map, const int32_t* offsets, int R,
-                        int C, int O, int E, int group_shift, int scale_rows, int x3d,
+                        int C, int O, int E, int group_shift, int scale_bytes, int x3d,
                         int n_pairs, uint16_t* y, int* err) {
   using G_ = Geo<BT>;
-  constexpr int XS = G_::XS, X_STAGE_BYTES = G_::X_STAGE_BYTES;
+  constexpr int KST = G_::KST, H = G_::H, WS = G_::WS;
+  constexpr int QW_BYTES = G_::QW_BYTES, W_STAGE_BYTES = G_::W_STAGE_BYTES;
+  constexpr int QW_ROW_BYTES = (DX ? KST : BW) * 4;  // a packed row of the weight tile
+  constexpr int SC_ROW_BYTES = (DX ? KST : BW) * 2;
   extern __shared__ uint8_t smem_raw[];
   // 1024-byte aligned base; the same offset in both CTAs, so that one MMA
   // descriptor and one barrier offset name the matching buffers of the pair
@@ -213,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int j = 0; j < WS; ++j) {
       mbar_init(&bar->wfull[j], 1);
-      mbar_init(&bar->wempty[j], 4);      // the four warps of the slot's group
+      mbar_init(&bar->wempty[j], 4 * H);  // the four warps of each of its groups
     }
     for (int j = 0; j < AS; ++j) {
       mbar_init(&bar->afull[j], 2 * 4);   // the slot's group warps in both CTAs
@@ -249,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   walk.list = reinterpret_cast<ListedTile*>(smem + LIST_OFF);
   walk.fill(THREADS);
   const int NT = walk.count();          // tiles of this cluster
-  const int KB = (C + BK - 1) / BK;     // stages per tile
+  const int KB = (C + KST - 1) / KST;   // stages per tile
   const int G = NT * KB;                // stages of this cluster, over all its tiles
   // the list is complete; both CTAs' barriers are initialised and TMEM is
   // allocated before any thread signals the other CTA
@@ -264,104 +272,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp == 0 || warp == 2) {
     // ---------------- TMA producers: X half (warp 0), weights (warp 2) ----------------
-    if (lane == 0 && NT > 0) {
-      int it = 0, kb = 0, o0;
-      ExpertTile tt = walk.at(0, rank, o0);
-      int s = 0;
-      uint32_t ph = 0;
-      int issued = 0;
+    // Converged warps; one elected lane issues.  The stage after is asked for
+    // before this one's copies are issued (see the MMA warp).
+    int kb = 0, it = 0, o0 = 0, s = 0, issued = 0;
+    uint32_t ph = 0;
+    ExpertTile tt{0, 0, 0, 32};
+    if (NT > 0) tt = walk.at(0, rank, o0);
+    bool ok = true, free = false;
+    uint64_t* const empty = warp == 0 ? bar->xempty : bar->wempty;
+    const int ring = warp == 0 ? XS : WS;
+    for (int g = 0; g < G; ++g) {
+      if (!free)
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, kWaitLimitNs));
+      if (!ok) {
+        if (lane == 0) record_timeout(err, bar);
+        break;
+      }
+      const int s1 = s + 1 < ring ? s + 1 : 0;
+      const uint32_t ph1 = s1 ? ph : ph ^ 1u;
+      const bool next = mbar_test_wait(smem_u32(&empty[s1]), ph1 ^ 1u);
+      const int c0 = kb * KST;
       if (warp == 0) {
         // The odd CTA's half of the token tile may lie wholly past the last
         // row of X: then it loads nothing and the even CTA expects only its
         // own bytes; the MMA reads stale shared memory for token columns that
         // are never stored.
-        int box = box_index(tt.n);
-        bool odd_rows = tt.row0 + tt.n / 2 < R;
-        int row = tt.row0 + (int)rank * (tt.n / 2);
-        for (int g = 0; g < G; ++g) {
-          if (!mbar_wait_bounded(&bar->xempty[s], ph ^ 1u, abort_flag, kWaitLimitNs)) {
-            record_timeout(err, bar);
-            break;
-          }
+        const int box = box_index(tt.n), row = tt.row0 + (int)rank * (tt.n / 2);
+        const bool odd_rows = tt.row0 + tt.n / 2 < R;
+        if (elect_one()) {
           uint8_t* dst = xs + s * X_STAGE_BYTES;
           const uint32_t bar_c = xfull_even + 8u * (uint32_t)s;
-          const uint32_t half_bytes = 4096u << box;
-          const int c0 = kb * BK;
-          // the second 64-column half holds columns below C (else it is
-          // neither loaded nor multiplied)
-          const bool hi = c0 + 64 < C;
+          const uint32_t atom_bytes = 4096u << box;
+          // atoms that hold columns below C (a 3-D box always fills all)
+          const int atoms = x3d ? G_::ATOMS : min(G_::ATOMS, (C - c0 + 63) / 64);
           if (even)
-            mbar_arrive_expect_tx(&bar->xfull[s],
-                                  (odd_rows ? 2u : 1u) * ((x3d || hi) ? 2 * half_bytes
-                                                                      : half_bytes));
+            mbar_arrive_expect_tx(&bar->xfull[s], (odd_rows ? 2u : 1u) * atoms * atom_bytes);
           if (even || odd_rows) {
             if (x3d) {
               tma_load_3d_pair(dst, &x_maps.rows[box], 0, row, c0 / 64, bar_c);
             } else {
-              tma_load_2d_pair(dst, &x_maps.rows[box], c0, row, bar_c);
-              if (hi)
-                tma_load_2d_pair(dst + half_bytes, &x_maps.rows[box], c0 + 64, row, bar_c);
-            }
-          }
-          ++issued;
-          if (++s == XS) {
-            s = 0;
-            ph ^= 1u;
-          }
-          if (++kb == KB) {
-            kb = 0;
-            if (++it < NT) {
-              tt = walk.at(it, rank, o0);
-              box = box_index(tt.n);
-              odd_rows = tt.row0 + tt.n / 2 < R;
-              row = tt.row0 + (int)rank * (tt.n / 2);
+              for (int a = 0; a < atoms; ++a)
+                tma_load_2d_pair(dst + a * atom_bytes, &x_maps.rows[box], c0 + 64 * a, row, bar_c);
             }
           }
         }
-        if (*abort_flag && even) {
-          // drain: wait for the last loads issued into each slot (the odd
-          // CTA's X loads complete on the even CTA's barriers, which the
-          // even CTA drains)
-          int never = 0;
-          for (int j = issued - 1; j >= 0 && j >= issued - XS; --j)
-            mbar_wait_bounded(&bar->xfull[j % XS], (uint32_t)(j / XS) & 1u, &never,
-                              kDrainLimitNs);
-        }
-      } else {
-        const uint32_t wbytes = QW_STAGE_BYTES + scale_rows * S_ROW_BYTES;
-        for (int g = 0; g < G; ++g) {
-          if (!mbar_wait_bounded(&bar->wempty[s], ph ^ 1u, abort_flag, kWaitLimitNs)) {
-            record_timeout(err, bar);
-            break;
-          }
-          uint8_t* wst = smem + W_OFF + s * W_STAGE_BYTES;
-          if (o0 < O) {
-            // first column and first k of the stage's weight tile
-            const int n0 = DX ? kb * BK : o0, k0 = DX ? o0 : kb * BK;
-            mbar_arrive_expect_tx(&bar->wfull[s], wbytes);
-            tma_load_3d(wst, &qw_map, n0, k0 / 8, tt.e, &bar->wfull[s]);
-            tma_load_3d(wst + QW_STAGE_BYTES, &s_map, n0, (int)((int64_t)k0 >> group_shift),
-                        tt.e, &bar->wfull[s]);
-          } else {
-            mbar_arrive(&bar->wfull[s]);  // padding CTA: no columns, nothing to load
-          }
-          ++issued;
-          if (++s == WS) {
-            s = 0;
-            ph ^= 1u;
-          }
-          if (++kb == KB) {
-            kb = 0;
-            if (++it < NT) tt = walk.at(it, rank, o0);
-          }
-        }
-        if (*abort_flag) {
-          int never = 0;
-          for (int j = issued - 1; j >= 0 && j >= issued - WS; --j)
-            mbar_wait_bounded(&bar->wfull[j % WS], (uint32_t)(j / WS) & 1u, &never,
-                              kDrainLimitNs);
+      } else if (elect_one()) {
+        uint8_t* wst = smem + W_OFF + s * W_STAGE_BYTES;
+        if (o0 < O) {
+          // first column and first k of the stage's weight tile
+          const int n0 = DX ? c0 : o0, k0 = DX ? o0 : c0;
+          mbar_arrive_expect_tx(&bar->wfull[s], QW_BYTES + scale_bytes);
+          tma_load_3d(wst, &qw_map, n0, k0 / 8, tt.e, &bar->wfull[s]);
+          tma_load_3d(wst + QW_BYTES, &s_map, n0, (int)((int64_t)k0 >> group_shift), tt.e,
+                      &bar->wfull[s]);
+        } else {
+          mbar_arrive(&bar->wfull[s]);  // padding CTA: no columns, nothing to load
         }
       }
+      __syncwarp();
+      free = __all_sync(0xffffffffu, next);
+      ++issued;
+      s = s1;
+      ph = ph1;
+      if (++kb == KB) {
+        kb = 0;
+        if (++it < NT) tt = walk.at(it, rank, o0);
+      }
+    }
+    if (*abort_flag && (even || warp == 2)) {
+      // drain: wait for the last loads issued into each slot (the odd CTA's X
+      // loads complete on the even CTA's barriers, which the even CTA drains)
+      int never = 0;
+      uint64_t* const full = warp == 0 ? bar->xfull : bar->wfull;
+      for (int i = issued - 1; i >= 0 && i >= issued - ring; --i)
+        mbar_wait_bounded(&full[i % ring], (uint32_t)(i / ring) & 1u, &never, kDrainLimitNs);
     }
     __syncwarp();  // the whole warp reaches the cluster barrier below together
   } else if (warp == 1) {
@@ -375,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int o0;
         const int n = walk.at(it, rank, o0).n;
         const uint32_t idesc = idesc_f16_f32(2 * BW, n);
-        const uint32_t half_bytes = 4096u << box_index(n);
+        const uint32_t atom_bytes = 4096u << box_index(n);
         const uint32_t d = tmem + D_COL + (n <= (int)D_HALF ? (it & 1) * D_HALF : 0u);
         // the tile before the last has been read out; the last one too, where
         // the two share accumulator columns
@@ -390,112 +375,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         last_n = n;
-        // With small tiles two stages at a time where there are two: the warp's
-        // own waits and commits cost as much as a small tile's MMAs.  (With 256
-        // tokens waiting for two of the three X stages costs more than it saves.)
-        constexpr int TURN = BT <= 128 ? 2 : 1;
-        for (int kb = 0; kb < KB; kb += TURN) {
-          const bool two = TURN == 2 && kb + 1 < KB;
-          const int s1 = s + 1 < XS ? s + 1 : 0, a1 = a + 1 < AS ? a + 1 : 0;
-          const uint32_t xph1 = s1 ? xph : xph ^ 1u, aph1 = a1 ? aph : aph ^ 1u;
+        for (int kb = 0; kb < KB; ++kb) {
+          // the stage's A slots: a, and with two per stage a + 1 (a is even then)
           if (!ready)
-            ok = __all_sync(
-                0xffffffffu,
-                mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
-                    mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
-                    (!two ||
-                     (mbar_wait_bounded(&bar->xfull[s1], xph1, abort_flag, kWaitLimitNs) &&
-                      mbar_wait_bounded(&bar->afull[a1], aph1, abort_flag, kWaitLimitNs))));
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                                mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
+                                (H == 1 || mbar_wait_bounded(&bar->afull[a + H - 1], aph,
+                                                             abort_flag, kWaitLimitNs)));
           if (!ok) break;
           tc_fence_after();
-          // Are the next two there already?  Asked before these MMAs are issued
+          // Is the next stage there already?  Asked before these MMAs are issued
           // and answered after: a wait that has nothing to wait for still costs
           // 200 cycles here.
-          int s2 = s1, a2 = a1;
-          uint32_t xph2 = xph1, aph2 = aph1;
-          if (two) {
-            s2 = s1 + 1 < XS ? s1 + 1 : 0;
-            a2 = a1 + 1 < AS ? a1 + 1 : 0;
-            xph2 = s2 ? xph1 : xph1 ^ 1u;
-            aph2 = a2 ? aph1 : aph1 ^ 1u;
-          }
-          bool next = mbar_test_wait(smem_u32(&bar->xfull[s2]), xph2) &
-                      mbar_test_wait(smem_u32(&bar->afull[a2]), aph2);
-          if (TURN == 2) {
-            const int s3 = s2 + 1 < XS ? s2 + 1 : 0, a3 = a2 + 1 < AS ? a2 + 1 : 0;
-            next &= mbar_test_wait(smem_u32(&bar->xfull[s3]), s3 ? xph2 : xph2 ^ 1u) &
-                    mbar_test_wait(smem_u32(&bar->afull[a3]), a3 ? aph2 : aph2 ^ 1u);
-          }
-          // the stage's MMAs; k16 steps that hold columns below C
-          const auto issue = [&](int sx, int ax, int kbx) {
-            const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + sx * X_STAGE_BYTES));
-            const uint64_t b_hi = b_lo + (uint64_t)(half_bytes >> 4);
-            const uint32_t a_base = tmem + A_COL + ax * A_STAGE_COLS;
-            const int nk = min(BK, C - kbx * BK + 15) / 16;
-            const uint32_t keep = kbx > 0 ? 1u : 0u;
-            if (nk == BK / 16) {
-#pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk)
-                mma_f16_ts_pair(d, a_base + kk * 8,
-                                (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
-                                kk > 0 ? 1u : keep);
-            } else {
-#pragma unroll 1
-              for (int kk = 0; kk < nk; ++kk)
-                mma_f16_ts_pair(d, a_base + kk * 8,
-                                (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
-                                kk > 0 ? 1u : keep);
-            }
-            mma_commit_pair(&bar->xempty[sx], kPairMask);
-            mma_commit_pair(&bar->aempty[ax], kPairMask);
-          };
+          const int s1 = s + 1 < XS ? s + 1 : 0, a1 = a + H < AS ? a + H : 0;
+          const uint32_t xph1 = s1 ? xph : xph ^ 1u, aph1 = a1 ? aph : aph ^ 1u;
+          bool next = mbar_test_wait(smem_u32(&bar->xfull[s1]), xph1) &
+                      mbar_test_wait(smem_u32(&bar->afull[a1]), aph1);
+          if (H == 2) next &= mbar_test_wait(smem_u32(&bar->afull[a1 + 1]), aph1);
           if (elect_one()) {
-            issue(s, a, kb);
-            if (two) issue(s1, a1, kb + 1);
-            if (kb + TURN >= KB) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+              const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES)) +
+                                    (uint64_t)((2 * h * atom_bytes) >> 4);
+              const uint64_t b_hi = b_lo + (uint64_t)(atom_bytes >> 4);
+              const uint32_t a_base = tmem + A_COL + (a + h) * A_STAGE_COLS;
+              // k16 steps that hold columns below C
+              const int nk = min(BK, C - kb * KST - h * BK + 15) / 16;
+              const uint32_t keep = kb > 0 || h > 0 ? 1u : 0u;
+              if (nk == BK / 16) {
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                  mma_f16_ts_pair(d, a_base + kk * 8,
+                                  (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4),
+                                  idesc, kk > 0 ? 1u : keep);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk < nk; ++kk)
+                  mma_f16_ts_pair(d, a_base + kk * 8,
+                                  (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4),
+                                  idesc, kk > 0 ? 1u : keep);
+              }
+              mma_commit_pair(&bar->aempty[a + h], kPairMask);
+            }
+            mma_commit_pair(&bar->xempty[s], kPairMask);
+            if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
           }
           __syncwarp();
           ready = __all_sync(0xffffffffu, next);
-          s = s2;
-          a = a2;
-          xph = xph2;
-          aph = aph2;
+          s = s1;
+          a = a1;
+          xph = xph1;
+          aph = aph1;
         }
       }
       if (!ok) {
         if (lane == 0) record_timeout(err, bar);
         // wait for the MMAs already issued before anyone frees TMEM
-        if (elect_one()) mma_commit_pair(&bar->aempty[a], kPairMask);
+        if (elect_one()) mma_commit_pair(&bar->aempty[a + H - 1], kPairMask);
         __syncwarp();
         int never = 0;
-        mbar_wait_bounded(&bar->aempty[a], aph, &never, kDrainLimitNs);
+        mbar_wait_bounded(&bar->aempty[a + H - 1], aph, &never, kDrainLimitNs);
       }
     }
     __syncwarp();  // the whole warp reaches the cluster barrier below together
   } else if (warp < EPI_WARP0) {
     // ---------------- dequantisation ----------------
     const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
-    const int j = (warp - DQ_WARP0) >> 2;    // group: stages g = j mod 4, A slot j
+    const int j = (warp - DQ_WARP0) >> 2;    // group: slots' worth f = j mod 4, A slot j
     const uint32_t a_slot =
         tmem + ((uint32_t)(32 * quarter) << 16) + A_COL + j * A_STAGE_COLS;
     // forward: this thread's column in weight slot 0; gradient: its packed
     // row, its four columns of every sixteen, and its half of their words
     const int col = 32 * quarter + 4 * (lane & 7) + (lane >> 3);
     const int prow = 4 * quarter + (lane >> 3);
-    const uint8_t* qw0 =
-        smem + W_OFF + (DX ? prow * QW_ROW_BYTES + (lane & 3) * 16 : col * 4);
+    // ... in its half of a stage
+    const int hf = j % H;
+    const uint8_t* qw0 = smem + W_OFF +
+                         (DX ? prow * QW_ROW_BYTES + (BK * hf + 4 * (lane & 3)) * 4
+                             : BK / 8 * hf * QW_ROW_BYTES + col * 4);
+    const int gs = min(group_shift, 30);
     const uint8_t* sc0 =
-        smem + W_OFF + QW_STAGE_BYTES +
-        (DX ? (group_shift >= 7 ? 0 : (prow * 8) >> group_shift) * S_ROW_BYTES + (lane & 3) * 8
-            : col * 2);
+        smem + W_OFF + QW_BYTES +
+        (DX ? (gs >= 7 ? 0 : (prow * 8) >> gs) * SC_ROW_BYTES + (BK * hf + 4 * (lane & 3)) * 2
+            : ((BK * hf) >> gs) * SC_ROW_BYTES + col * 2);
     const uint32_t half = (uint32_t)(lane >> 2) & 1u;  // k 0..3 or 4..7 of the words
     const uint32_t pick_lo = half ? 0x6622u : 0x4400u;  // first byte of two words' halves
     const uint32_t pick_hi = half ? 0x7733u : 0x5511u;  // second byte
 
     bool ok = true;
-    int jw = j;                  // weight slot and its phase
+    int jw = j / H;              // weight stage's slot and its phase
     uint32_t pw = 0, ph = 0;     // ... and the A slot's
-    for (int g = j; g < G; g += DQ_GROUPS) {
+    for (int g = j; g < G * H; g += DQ_GROUPS) {
       const uint8_t* qw = qw0 + jw * W_STAGE_BYTES;
       const uint8_t* sc = sc0 + jw * W_STAGE_BYTES;
       // qweight and scale tiles of the stage have landed
@@ -508,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int r = 0; r < BK / 8; r += WPS)
           small = small && scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
-                               sc + r / WPS * S_ROW_BYTES));
+                               sc + r / WPS * SC_ROW_BYTES));
         small = __all_sync(0xffffffffu, small);
       }
       // the stage's 128 k (or n), one half (32 TMEM columns) at a time
@@ -547,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int r0 = 0; r0 < 8; r0 += PER) {
             const uint32_t s2 = half2_broadcast(*reinterpret_cast<const uint16_t*>(
-                sc + (8 * h + r0) / WPS * S_ROW_BYTES));
+                sc + (8 * h + r0) / WPS * SC_ROW_BYTES));
             if (small) {
               uint32_t b2, c2;
               subnormal_form_constants(s2, b2, c2);
@@ -583,7 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(afull_even + 8u * (uint32_t)j);
       ph ^= 1u;
-      jw += DQ_GROUPS;
+      jw += DQ_GROUPS / H;
       if (jw >= WS) {
         jw -= WS;
         pw ^= 1u;
@@ -694,18 +665,23 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
   const int64_t C = DX ? N : K, O = DX ? K : N;
   const int64_t n_groups = (group_shift == 62 || (int64_t(1) << group_shift) >= K)
                                ? 1 : (K + (int64_t(1) << group_shift) - 1) >> group_shift;
-  const int scale_rows = group_shift >= 7 ? 1 : (BK >> group_shift);
+  using G_ = Geo<BT>;
+  // scale rows that a stage's k touch (KST of them, or the CTA's 128 in the
+  // gradient), and its columns
+  const int span = DX ? BW : G_::KST;
+  const int scale_rows = group_shift >= 30 || (span >> group_shift) < 1 ? 1 : span >> group_shift;
+  const int scale_cols = DX ? G_::KST : BW;
   XMaps x_maps;
   CUtensorMap qw_map, s_map, y_map;
-  // X as [C/64][R][64] (one copy of both 64-column halves per stage) when C is
-  // a multiple of 64, else as [R][C] (one copy per half); rows at or beyond R
+  // X as [C/64][R][64] (one copy of all the 64-column atoms per stage) when C
+  // is a multiple of 64, else as [R][C] (one copy per atom); rows at or beyond R
   // and columns at or beyond C read as zero either way
   const int x3d = C % 64 == 0;
   for (int i = 0; i < 3; ++i) {
     const uint32_t rows = 32u << i;
     const uint64_t dims[3] = {64, (uint64_t)R, (uint64_t)(C / 64)};
     const uint64_t strides[2] = {(uint64_t)C * 2, 128};
-    const uint32_t box[3] = {64, rows, 2};
+    const uint32_t box[3] = {64, rows, G_::ATOMS};
     if (!(x3d ? encode_map_3d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides,
                               box, CU_TENSOR_MAP_SWIZZLE_128B)
               : encode_map_2d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)C,
@@ -714,10 +690,10 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
   }
   const uint64_t qdims[3] = {(uint64_t)N, (uint64_t)(K / 8), (uint64_t)E};
   const uint64_t qstrides[2] = {(uint64_t)N * 4, (uint64_t)(K / 8) * N * 4};
-  const uint32_t qbox[3] = {BW, BK / 8, 1};
+  const uint32_t qbox[3] = {(uint32_t)scale_cols, (uint32_t)span / 8, 1};
   const uint64_t sdims[3] = {(uint64_t)N, (uint64_t)n_groups, (uint64_t)E};
   const uint64_t sstrides[2] = {(uint64_t)N * 2, (uint64_t)n_groups * N * 2};
-  const uint32_t sbox[3] = {BW, (uint32_t)scale_rows, 1};
+  const uint32_t sbox[3] = {(uint32_t)scale_cols, (uint32_t)scale_rows, 1};
   if (!encode_map_3d(&qw_map, qweight, CU_TENSOR_MAP_DATA_TYPE_INT32, qdims, qstrides, qbox,
                      CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_map_3d(&s_map, scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, sdims, sstrides, sbox,
@@ -753,7 +729,8 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, experts_pair_kernel<DX, BT, WPS>, x_maps, qw_map, s_map, y_map, offsets,
-                            (int)R, (int)C, (int)O, (int)E, group_shift, scale_rows, x3d,
+                            (int)R, (int)C, (int)O, (int)E, group_shift,
+                            scale_rows * scale_cols * 2, x3d,
                             (int)n_pairs, y, dev.error_word);
 }
 
