@@ -241,11 +241,20 @@ int status_of(cudaError_t e) {
 }
 
 // The kernel of the experts' products, and its token tile, from the rows an
-// expert has on average.
+// expert has on average.  Measured (us; tiles of 8 / 16 / 32 on the decode
+// kernel, then the pair kernel) with 64 experts of 2048 x 2048 at 1, 4, 8 and
+// 16 rows: 28 / 28 / 29 / 32, 40 / 36 / 39 / 41, 58 / 45.5 / 45.0 / 46.2 and
+// 86 / 61 / 52 / 47; with 8 experts of 5120 x 17408 at 1, 4, 8 and 16 rows:
+// 69 / 69 / 77 / 84, 95 / 90 / 94 / 109, 127 / 96 / 97 / 109 and 197 / 129 /
+// 101 / 110.
 int select_experts_kernel(int64_t R, int64_t E, int32_t* tile) {
   const int64_t mean = (R + E - 1) / E;
-  *tile = mean <= 2 ? 8 : mean <= 6 ? 16 : mean <= 16 ? 32 : 64;
-  return mean <= 40 ? GPTQ_KERNEL_DECODE : GPTQ_KERNEL_PREFILL;
+  if (mean > 10) {
+    *tile = 0;
+    return GPTQ_KERNEL_PREFILL;
+  }
+  *tile = mean <= 1 ? 8 : mean <= 5 ? 16 : 32;
+  return GPTQ_KERNEL_DECODE;
 }
 
 // The experts' products: in [R, K] -> out [R, N], or the gradient in [R, N]
@@ -257,7 +266,7 @@ int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* sca
   int st = check_shape(R, K, N, group);
   if (st != GPTQ_OK) return st;
   if (kernel_id < GPTQ_KERNEL_AUTO || kernel_id > GPTQ_KERNEL_PREFILL) return GPTQ_ERR_KERNEL;
-  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 8 && tile != 16 && tile != 32 && tile != 64 : tile != 0)
+  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 8 && tile != 16 && tile != 32 : tile != 0)
     return GPTQ_ERR_KERNEL;
   if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
   if (!qweight || !scales || !offsets) return GPTQ_ERR_NULL;

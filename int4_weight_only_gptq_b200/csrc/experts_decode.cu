@@ -65,7 +65,7 @@ constexpr int QW_ROW_BYTES = BW * 4;
 constexpr int S_ROW_BYTES = BW * 2;
 constexpr int kMaxStages = 8;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t D_COL = 0;     // two accumulators of up to 64 columns
+constexpr uint32_t D_COL = 0;     // two accumulators of up to 32 columns
 constexpr uint32_t D_NEXT = 64;
 constexpr uint32_t A_COL = 128;   // A slots: [128, 512), 128 columns each
 constexpr uint32_t A_SLOT_COLS = BK / 2;
@@ -597,8 +597,7 @@ cudaError_t launch_experts_decode(const uint16_t* x, const int32_t* qweight,
                                   int tile, cudaStream_t stream, const DeviceInfo& dev) {
   const auto launch = tile <= 8    ? launch_rows<8>
                       : tile <= 16 ? launch_rows<16>
-                      : tile <= 32 ? launch_rows<32>
-                                   : launch_rows<64>;
+                                   : launch_rows<32>;
   return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
 }
 
