@@ -381,28 +381,42 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     return out
 
 
-def _require_moe(t, name: str, dtype, device, shape=None):
-    """The checks of _require and _check_shape in one pass: the calls of a
-    decoding step last a few microseconds on the device, so their checks are
-    kept short."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_cuda
-            and t.device == device and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
-        _require(t, name, lambda d: d == dtype, device)
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+# The calls of a decoding step's experts last a few microseconds on the device,
+# about as long as a call takes on the host, so their checks are kept short:
+# one expression per tensor, device indices instead of device objects, the
+# stream's handle without the stream object.
+
+def _bad(t, name: str, dtype, index: int, shape=None):
+    """Raises for a tensor that _fits refused, in _require's words."""
+    _require(t, name, lambda d: d == dtype, torch.device("cuda", index))
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _call(fn, device, stream, *args):
+def _fits(t, dtype, index: int) -> bool:
+    """A contiguous CUDA tensor of this type on this device."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous())
+
+
+def _device_index(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(fn, index: int, stream, *args):
     """fn(*args, stream) with the tensors' device current."""
     if stream is None:
-        # the handle of torch.cuda.current_stream(device), without the object
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
+        # the handle of torch.cuda.current_stream(index), without the object
+        stream = torch._C._cuda_getCurrentRawStream(index)
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             status = fn(*args, stream)
     if status != 0:
         _check(status)
@@ -418,24 +432,29 @@ def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
     int32): expert e's rows are offsets[e] .. offsets[e + 1] - 1, choice j of
     token m is row dest[m, j] (-1 if dropped), in the order of (m, j) within an
     expert.  The rows from offsets[n_experts] on keep what `out` holds."""
-    lib = load()
-    dev = x.device
-    _require_moe(x, "x", torch.float16, dev)
-    id_dtype = torch.int64 if expert_ids.dtype == torch.int64 else torch.int32
-    _require_moe(expert_ids, "expert_ids", id_dtype, dev)
-    if x.dim() != 2 or expert_ids.dim() != 2 or expert_ids.shape[0] != x.shape[0]:
-        raise ValueError("x and expert_ids must be 2-D with one row per token")
+    lib = _lib or load()
+    dev = _device_index(x, "x")
+    if not _fits(x, torch.float16, dev):
+        _bad(x, "x", torch.float16, dev)
+    wide = isinstance(expert_ids, torch.Tensor) and expert_ids.dtype is torch.int64
+    id_dtype = torch.int64 if wide else torch.int32
+    if not _fits(expert_ids, id_dtype, dev):
+        _bad(expert_ids, "expert_ids", id_dtype, dev)
+    if x.dim() != 2 or expert_ids.dim() != 2:
+        raise ValueError("x and expert_ids must be 2-D")
     M, H = x.shape
-    topk = expert_ids.shape[1]
+    tokens, topk = expert_ids.shape
+    if tokens != M:
+        raise ValueError(f"expert_ids has {tokens} rows, expected one per token ({M})")
     if out is None:
-        out = torch.empty((M * topk, H), dtype=torch.float16, device=dev)
-    else:
-        _require_moe(out, "out", torch.float16, dev, (M * topk, H))
-    offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=dev)
-    dest = torch.empty((M, topk), dtype=torch.int32, device=dev)
-    _call(lib.gptq_moe_sort, dev, stream, x.data_ptr(), expert_ids.data_ptr(),
-          8 if id_dtype == torch.int64 else 4, M, H, topk, n_experts, out.data_ptr(),
-          offsets.data_ptr(), dest.data_ptr())
+        out = torch.empty((M * topk, H), dtype=torch.float16, device=x.device)
+    elif not _fits(out, torch.float16, dev) or out.shape != (M * topk, H):
+        _bad(out, "out", torch.float16, dev, (M * topk, H))
+    offsets = x.new_empty(n_experts + 1 if n_experts > 0 else 1, dtype=torch.int32)
+    dest = (torch.empty_like(expert_ids, dtype=torch.int32) if wide
+            else torch.empty_like(expert_ids))
+    _call(lib.gptq_moe_sort, dev, stream, x.data_ptr(), expert_ids.data_ptr(), 8 if wide else 4,
+          M, H, topk, n_experts, out.data_ptr(), offsets.data_ptr(), dest.data_ptr())
     return out, offsets, dest
 
 
@@ -445,20 +464,23 @@ def moe_combine(y_sorted: torch.Tensor, dest: torch.Tensor, weights: torch.Tenso
     the order of j, dropped choices (dest -1) left out.  y_sorted [R, H] FP16,
     dest [M, topk] int32 from moe_sort, weights [M, topk] FP32 or None for
     ones (then it is moe_sort's gradient, applied to that of x_sorted)."""
-    lib = load()
-    dev = y_sorted.device
-    _require_moe(y_sorted, "y_sorted", torch.float16, dev)
-    _require_moe(dest, "dest", torch.int32, dev)
+    lib = _lib or load()
+    dev = _device_index(y_sorted, "y_sorted")
+    if not _fits(y_sorted, torch.float16, dev):
+        _bad(y_sorted, "y_sorted", torch.float16, dev)
+    if not _fits(dest, torch.int32, dev):
+        _bad(dest, "dest", torch.int32, dev)
     if y_sorted.dim() != 2 or dest.dim() != 2:
         raise ValueError("y_sorted and dest must be 2-D")
     M, topk = dest.shape
     R, H = y_sorted.shape
-    if weights is not None:
-        _require_moe(weights, "weights", torch.float32, dev, (M, topk))
+    if weights is not None and (not _fits(weights, torch.float32, dev)
+                                or weights.shape != dest.shape):
+        _bad(weights, "weights", torch.float32, dev, (M, topk))
     if out is None:
-        out = torch.empty((M, H), dtype=torch.float16, device=dev)
-    else:
-        _require_moe(out, "out", torch.float16, dev, (M, H))
+        out = torch.empty((M, H), dtype=torch.float16, device=y_sorted.device)
+    elif not _fits(out, torch.float16, dev) or out.shape != (M, H):
+        _bad(out, "out", torch.float16, dev, (M, H))
     _call(lib.gptq_moe_combine, dev, stream, y_sorted.data_ptr(), dest.data_ptr(),
           None if weights is None else weights.data_ptr(), M, H, topk, R, out.data_ptr())
     return out
@@ -470,23 +492,27 @@ def moe_combine_backward(dout: torch.Tensor, y_sorted: torch.Tensor, dest: torch
     dweights [M, topk] FP32) from dout [M, H] FP16.  Rows that no entry of dest
     names keep what `out` (the buffer of dy_sorted) holds; dweights is 0 for
     dropped choices."""
-    lib = load()
-    dev = dout.device
-    _require_moe(dout, "dout", torch.float16, dev)
-    _require_moe(y_sorted, "y_sorted", torch.float16, dev)
-    _require_moe(dest, "dest", torch.int32, dev)
+    lib = _lib or load()
+    dev = _device_index(dout, "dout")
+    if not _fits(dout, torch.float16, dev):
+        _bad(dout, "dout", torch.float16, dev)
+    if not _fits(y_sorted, torch.float16, dev):
+        _bad(y_sorted, "y_sorted", torch.float16, dev)
+    if not _fits(dest, torch.int32, dev):
+        _bad(dest, "dest", torch.int32, dev)
     if dout.dim() != 2 or y_sorted.dim() != 2 or dest.dim() != 2:
         raise ValueError("dout, y_sorted and dest must be 2-D")
     M, topk = dest.shape
     R, H = y_sorted.shape
     if dout.shape != (M, H):
         raise ValueError(f"dout has shape {tuple(dout.shape)}, expected {(M, H)}")
-    _require_moe(weights, "weights", torch.float32, dev, (M, topk))
+    if not _fits(weights, torch.float32, dev) or weights.shape != dest.shape:
+        _bad(weights, "weights", torch.float32, dev, (M, topk))
     if out is None:
-        out = torch.empty((R, H), dtype=torch.float16, device=dev)
-    else:
-        _require_moe(out, "out", torch.float16, dev, (R, H))
-    dweights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+        out = torch.empty_like(y_sorted)
+    elif not _fits(out, torch.float16, dev) or out.shape != y_sorted.shape:
+        _bad(out, "out", torch.float16, dev, (R, H))
+    dweights = torch.empty_like(weights)
     _call(lib.gptq_moe_combine_backward, dev, stream, dout.data_ptr(), y_sorted.data_ptr(),
           dest.data_ptr(), weights.data_ptr(), M, H, topk, R, out.data_ptr(),
           dweights.data_ptr())
@@ -501,7 +527,8 @@ def experts_shapes(rows, qweight, scales, offsets, group: int,
     left to the library."""
     if rows.dim() != 2 or qweight.dim() != 3 or scales.dim() != 3 or offsets.dim() != 1:
         raise ValueError("need 2-D rows, 3-D qweight and scales, 1-D offsets")
-    E, K, N = qweight.shape[0], 8 * qweight.shape[1], qweight.shape[2]
+    E, packed, N = qweight.shape
+    K = 8 * packed
     R, width = rows.shape
     if width != (N if gradient else K):
         raise ValueError(f"rows have {width} columns, expected {N if gradient else K}")
@@ -516,17 +543,21 @@ def experts_shapes(rows, qweight, scales, offsets, group: int,
 def _experts(fn, rows, qweight, scales, offsets, group, out, stream, gradient, name):
     """Checks and output of an experts' product, and its library call; `fn`
     takes the entry's arguments without the kernel choice."""
-    dev = qweight.device
-    _require_moe(qweight, "qweight", torch.int32, dev)
-    _require_moe(scales, "scales", torch.float16, dev)
-    _require_moe(offsets, "offsets", torch.int32, dev)
-    _require_moe(rows, name, torch.float16, dev)
+    dev = _device_index(qweight, "qweight")
+    if not _fits(qweight, torch.int32, dev):
+        _bad(qweight, "qweight", torch.int32, dev)
+    if not _fits(scales, torch.float16, dev):
+        _bad(scales, "scales", torch.float16, dev)
+    if not _fits(offsets, torch.int32, dev):
+        _bad(offsets, "offsets", torch.int32, dev)
+    if not _fits(rows, torch.float16, dev):
+        _bad(rows, name, torch.float16, dev)
     R, K, N, E = experts_shapes(rows, qweight, scales, offsets, group, gradient)
     shape = (R, K if gradient else N)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float16, device=dev)
-    else:
-        _require_moe(out, "out", torch.float16, dev, shape)
+        out = torch.empty(shape, dtype=torch.float16, device=rows.device)
+    elif not _fits(out, torch.float16, dev) or out.shape != shape:
+        _bad(out, "out", torch.float16, dev, shape)
     _call(fn, dev, stream, rows.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
           offsets.data_ptr(), R, K, N, E, group, out.data_ptr())
     return out
@@ -541,7 +572,7 @@ def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     qweight [E, K/8, N] int32, scales [E, n_groups, N] FP16.  Rows that belong
     to no expert keep what `out` holds.  kernel and tile force the kernel: tests
     and benchmarks (KERNEL_DECODE takes a tile of 8, 16 or 32 rows)."""
-    lib = load()
+    lib = _lib or load()
     fn = lib.gptq_w4a16_gemm_experts
     if kernel != KERNEL_AUTO or tile != 0:
         fn = lambda *args: lib.gptq_w4a16_gemm_experts_kernel(*args, kernel, tile)
@@ -554,7 +585,7 @@ def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torc
     """The gradient of gemm_experts with respect to x_sorted: dx_sorted[r] =
     dy_sorted[r] . dequant(qweight[e], scales[e])^T, [R, K] FP16 from dy_sorted
     [R, N] FP16 (the packed weights are frozen and have no gradient)."""
-    return _experts(load().gptq_w4a16_gemm_experts_dx, dy_sorted, qweight, scales, offsets,
+    return _experts((_lib or load()).gptq_w4a16_gemm_experts_dx, dy_sorted, qweight, scales, offsets,
                     group, out, stream, True, "dy_sorted")
 
 
