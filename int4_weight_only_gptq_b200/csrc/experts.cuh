@@ -89,8 +89,8 @@ struct ExpertTable {
       if (tile[mid] <= t) lo = mid;
       else hi = mid;
     }
-    const int w = width(rows[lo]), at = (t - tile[lo]) * w;
-    return ExpertTile{lo, row[lo] + at, min(w, rows[lo] - at), w};
+    const int w = width(rows[lo]), at = (t - tile[lo]) * w, r = min(w, rows[lo] - at);
+    return ExpertTile{lo, row[lo] + at, r, (r + STEP - 1) / STEP * STEP};
   }
 };
 

@@ -295,7 +295,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tm = (uint32_t)uniform((int)tmem);
     bool ok = true;
     int s = 0, a = 0, use = 0;
-    bool ready = false;  // the next stage's A slot was seen to be written
     for (int j = 0; j < count && ok; ++j) {
       const uint32_t d = tm + D_COL + (uint32_t)(j & 1) * D_NEXT;
       if (j >= 2) {
@@ -306,17 +305,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (int t = 0; t < n_st; ++t) {
         // the stage's X has landed too: its A slot was written from the stage
-        if (!ready)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag,
-                                            kWaitLimitNs));
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag,
+                                          kWaitLimitNs));
         if (!ok) break;
         tc_fence_after();
-        // Is the next one written already?  Asked before this stage's MMAs are
-        // issued and answered after: a wait that has nothing to wait for still
-        // costs 200 cycles.
-        const int a1 = a + 1 < SLOTS ? a + 1 : 0, use1 = a1 ? use : use + 1;
-        const bool next = mbar_test_wait(smem_u32(&bar->afull[a1]), (uint32_t)use1 & 1u);
         const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
         const uint32_t a_base = tm + A_COL + a * A_SLOT_COLS;
         const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
@@ -340,9 +333,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (t == n_st - 1) mma_commit(&bar->dfull[j & 1]);
         }
         __syncwarp();
-        ready = __all_sync(0xffffffffu, next);
-        a = a1;
-        use = use1;
+        if (++a == SLOTS) {
+          a = 0;
+          ++use;
+        }
         if (++s == stages) s = 0;
       }
     }

@@ -272,26 +272,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp == 0 || warp == 2) {
     // ---------------- TMA producers: X half (warp 0), weights (warp 2) ----------------
-    // Converged warps; one elected lane issues.  The stage after is asked for
-    // before this one's copies are issued (see the MMA warp).
+    // Converged warps; one elected lane issues.
     int kb = 0, it = 0, o0 = 0, s = 0, issued = 0;
     uint32_t ph = 0;
     ExpertTile tt{0, 0, 0, 32};
     if (NT > 0) tt = walk.at(0, rank, o0);
-    bool ok = true, free = false;
+    bool ok = true;
     uint64_t* const empty = warp == 0 ? bar->xempty : bar->wempty;
     const int ring = warp == 0 ? XS : WS;
     for (int g = 0; g < G; ++g) {
-      if (!free)
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, kWaitLimitNs));
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, kWaitLimitNs));
       if (!ok) {
         if (lane == 0) record_timeout(err, bar);
         break;
       }
-      const int s1 = s + 1 < ring ? s + 1 : 0;
-      const uint32_t ph1 = s1 ? ph : ph ^ 1u;
-      const bool next = mbar_test_wait(smem_u32(&empty[s1]), ph1 ^ 1u);
       const int c0 = kb * KST;
       if (warp == 0) {
         // The odd CTA's half of the token tile may lie wholly past the last
@@ -331,10 +326,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       __syncwarp();
-      free = __all_sync(0xffffffffu, next);
       ++issued;
-      s = s1;
-      ph = ph1;
+      if (++s == ring) {
+        s = 0;
+        ph ^= 1u;
+      }
       if (++kb == KB) {
         kb = 0;
         if (++it < NT) tt = walk.at(it, rank, o0);
@@ -355,7 +351,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       int it = 0, s = 0, a = 0, last_n = 0;
       uint32_t xph = 0, aph = 0;
-      bool ready = false;  // the next stage's operands were seen to be there
       for (; it < NT && ok; ++it) {
         int o0;
         const int n = walk.at(it, rank, o0).n;
@@ -377,7 +372,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         last_n = n;
         for (int kb = 0; kb < KB; ++kb) {
           // the stage's A slots: a, and with two per stage a + 1 (a is even then)
-          if (!ready)
+          // All of them are asked at once first: waits that have nothing to wait
+          // for, one after the other, cost 200 cycles each under load, half the
+          // time of a small tile's stage.
+          bool there = mbar_test_wait(smem_u32(&bar->xfull[s]), xph) &
+                       mbar_test_wait(smem_u32(&bar->afull[a]), aph);
+          if (H == 2) there &= mbar_test_wait(smem_u32(&bar->afull[a + H - 1]), aph);
+          if (!__all_sync(0xffffffffu, there))
             ok = __all_sync(0xffffffffu,
                             mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
                                 mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
@@ -385,14 +386,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                                              abort_flag, kWaitLimitNs)));
           if (!ok) break;
           tc_fence_after();
-          // Is the next stage there already?  Asked before these MMAs are issued
-          // and answered after: a wait that has nothing to wait for still costs
-          // 200 cycles here.
-          const int s1 = s + 1 < XS ? s + 1 : 0, a1 = a + H < AS ? a + H : 0;
-          const uint32_t xph1 = s1 ? xph : xph ^ 1u, aph1 = a1 ? aph : aph ^ 1u;
-          bool next = mbar_test_wait(smem_u32(&bar->xfull[s1]), xph1) &
-                      mbar_test_wait(smem_u32(&bar->afull[a1]), aph1);
-          if (H == 2) next &= mbar_test_wait(smem_u32(&bar->afull[a1 + 1]), aph1);
           if (elect_one()) {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
@@ -422,11 +415,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
           }
           __syncwarp();
-          ready = __all_sync(0xffffffffu, next);
-          s = s1;
-          a = a1;
-          xph = xph1;
-          aph = aph1;
+          if (++s == XS) {
+            s = 0;
+            xph ^= 1u;
+          }
+          a += H;
+          if (a == AS) {
+            a = 0;
+            aph ^= 1u;
+          }
         }
       }
       if (!ok) {
