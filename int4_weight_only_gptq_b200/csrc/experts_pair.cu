@@ -14,8 +14,9 @@
 //   takes tiles c, c + clusters, ..., column pair fastest.
 // * A tile holds up to BT = 128 or 256 rows of one expert; the MMA's width is
 //   the rows rounded up to 32, so an expert with few rows pays for those only.
-//   The copy boxes of X come in 32, 64 and 128 rows per CTA for the same
-//   reason.  Rows that a box reads past the tile belong to other experts (or
+//   The copy box of X has half as many rows per CTA (a tensor map for each
+//   width): up to 128 tokens, L2 reads of X are what bounds the kernel.  Rows
+//   that a box reads past the tile belong to other experts (or
 //   read as zero past the tensor): each is a column of the accumulator of its
 //   own, which is never stored.
 // * Four warps of their own read a finished accumulator out.  Tiles of up to
@@ -128,12 +129,11 @@ struct PairBarriers {
 };
 static_assert(sizeof(PairBarriers) <= 512, "barrier area");
 
-// The boxes in which X is read: 32, 64 or 128 rows per CTA.
+// X in boxes of 16, 32, ... rows per CTA: half of each MMA width.
+template <int BT>
 struct XMaps {
-  CUtensorMap rows[3];
+  CUtensorMap width[BT / 32];
 };
-
-__device__ __forceinline__ int box_index(int n) { return n <= 64 ? 0 : (n <= 128 ? 1 : 2); }
 
 // The tiles of one cluster: tile = cluster + i * clusters for i = 0, 1, ...;
 // column pair fastest.  The first LISTED are looked up once, all threads at a
@@ -191,7 +191,7 @@ struct Walk {
 // for groups of 128 and more, 16; not used in the gradient).
 template <bool DX, int BT, int WPS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    experts_pair_kernel(const __grid_constant__ XMaps x_maps,
+    experts_pair_kernel(const __grid_constant__ XMaps<BT> x_maps,
                         const __grid_constant__ CUtensorMap qw_map,
                         const __grid_constant__ CUtensorMap s_map,
                         const __grid_constant__ CUtensorMap y_map, const int32_t* offsets, int R,
@@ -235,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     fence_mbarrier_init();
   }
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < 3; ++i) prefetch_tensormap(&x_maps.rows[i]);
+    for (int i = 0; i < BT / 32; ++i) prefetch_tensormap(&x_maps.width[i]);
     prefetch_tensormap(&qw_map);
     prefetch_tensormap(&s_map);
     prefetch_tensormap(&y_map);
@@ -293,22 +293,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // row of X: then it loads nothing and the even CTA expects only its
         // own bytes; the MMA reads stale shared memory for token columns that
         // are never stored.
-        const int box = box_index(tt.n), row = tt.row0 + (int)rank * (tt.n / 2);
+        const int row = tt.row0 + (int)rank * (tt.n / 2);
+        const CUtensorMap* x_map = &x_maps.width[tt.n / 32 - 1];
         const bool odd_rows = tt.row0 + tt.n / 2 < R;
         if (elect_one()) {
           uint8_t* dst = xs + s * X_STAGE_BYTES;
           const uint32_t bar_c = xfull_even + 8u * (uint32_t)s;
-          const uint32_t atom_bytes = 4096u << box;
+          const uint32_t atom_bytes = tt.n / 2 * 128;
           // atoms that hold columns below C (a 3-D box always fills all)
           const int atoms = x3d ? G_::ATOMS : min(G_::ATOMS, (C - c0 + 63) / 64);
           if (even)
             mbar_arrive_expect_tx(&bar->xfull[s], (odd_rows ? 2u : 1u) * atoms * atom_bytes);
           if (even || odd_rows) {
             if (x3d) {
-              tma_load_3d_pair(dst, &x_maps.rows[box], 0, row, c0 / 64, bar_c);
+              tma_load_3d_pair(dst, x_map, 0, row, c0 / 64, bar_c);
             } else {
               for (int a = 0; a < atoms; ++a)
-                tma_load_2d_pair(dst + a * atom_bytes, &x_maps.rows[box], c0 + 64 * a, row, bar_c);
+                tma_load_2d_pair(dst + a * atom_bytes, x_map, c0 + 64 * a, row, bar_c);
             }
           }
         }
@@ -355,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int o0;
         const int n = walk.at(it, rank, o0).n;
         const uint32_t idesc = idesc_f16_f32(2 * BW, n);
-        const uint32_t atom_bytes = 4096u << box_index(n);
+        const uint32_t atom_bytes = n / 2 * 128;
         const uint32_t d = tmem + D_COL + (n <= (int)D_HALF ? (it & 1) * D_HALF : 0u);
         // the tile before the last has been read out; the last one too, where
         // the two share accumulator columns
@@ -668,20 +669,20 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
   const int span = DX ? BW : G_::KST;
   const int scale_rows = group_shift >= 30 || (span >> group_shift) < 1 ? 1 : span >> group_shift;
   const int scale_cols = DX ? G_::KST : BW;
-  XMaps x_maps;
+  XMaps<BT> x_maps;
   CUtensorMap qw_map, s_map, y_map;
   // X as [C/64][R][64] (one copy of all the 64-column atoms per stage) when C
   // is a multiple of 64, else as [R][C] (one copy per atom); rows at or beyond R
   // and columns at or beyond C read as zero either way
   const int x3d = C % 64 == 0;
-  for (int i = 0; i < 3; ++i) {
-    const uint32_t rows = 32u << i;
+  for (int i = 0; i < BT / 32; ++i) {
+    const uint32_t rows = 16u * (i + 1);
     const uint64_t dims[3] = {64, (uint64_t)R, (uint64_t)(C / 64)};
     const uint64_t strides[2] = {(uint64_t)C * 2, 128};
     const uint32_t box[3] = {64, rows, G_::ATOMS};
-    if (!(x3d ? encode_map_3d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides,
+    if (!(x3d ? encode_map_3d(&x_maps.width[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides,
                               box, CU_TENSOR_MAP_SWIZZLE_128B)
-              : encode_map_2d(&x_maps.rows[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)C,
+              : encode_map_2d(&x_maps.width[i], x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (uint64_t)C,
                               (uint64_t)R, (uint64_t)C * 2, 64, rows, CU_TENSOR_MAP_SWIZZLE_128B)))
       return cudaErrorInvalidValue;
   }
