@@ -395,8 +395,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (WPS >= 4) {
 #pragma unroll
         for (int g = 0; g < PR / WPS; ++g)
-          small = small && scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
-                               sc + ((8 * WPS * g) >> gs) * S_ROW_BYTES));
+          small &= scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
+              sc + ((8 * WPS * g) >> gs) * S_ROW_BYTES));  // every load in flight at once
         small = __all_sync(0xffffffffu, small);
       }
       const uint32_t a_cells = a_lane + a * A_SLOT_COLS;

@@ -476,8 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         small = true;
 #pragma unroll
         for (int r = 0; r < BK / 8; r += WPS)
-          small = small && scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
-                               sc + r / WPS * SC_ROW_BYTES));
+          small &= scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
+              sc + r / WPS * SC_ROW_BYTES));  // every load in flight at once
         small = __all_sync(0xffffffffu, small);
       }
       // the stage's 128 k (or n), one half (32 TMEM columns) at a time
