@@ -7,17 +7,20 @@
 // from the experts' rows (experts.cuh) and one persistent CTA per SM walking
 // the (token tile, column block) items, column block fastest:
 //
-// * Ring stages of 256 k: the qweight box [32 packed rows x 128 columns]
-//   (16 KB), its scale rows and X [ROWS x 256 k], all by TMA.  Rows of X past
-//   the tile belong to other experts, each a column of the accumulator that is
-//   never stored.
+// * Two rings of 256-k stages, each with a producer warp: the qweight box [32
+//   packed rows x 128 columns] (16 KB) with its scale rows, freed as soon as
+//   its words are read, and X [ROWS x 256 k], freed by its MMAs.  (In one ring
+//   the weights stayed until the MMAs were done, and the loads in flight were
+//   too few.)  Rows of X past the tile belong to other experts, each a column of
+//   the accumulator that is never stored.
 // * Four groups of four warps take the stages in turn; stage f goes to TMEM A
 //   slot f mod 3: a thread turns the 32 words of its column into 128 cells.
 //   One wait for the stage, one for the slot and one arrival per 32 words: with
 //   sixteen words per warp between the barriers the waits were a third of all
 //   instructions.
-// * As in the decode kernel the words come out paired (k, k + 4), and the
-//   group permutes the tile's real X rows to the same order in place.
+// * Weights are written in natural k order (13 operations a word for scales
+//   below 2^-4).  The decode kernel's paired order needs 11, and X permuted in
+//   place with a fence for the tensor cores: no faster here.
 // * One elected lane issues the MMAs into one of two accumulators; four warps
 //   of their own read a finished item out and store it while the next one is
 //   multiplied.  (An MMA of 16 tokens takes 15 cycles, into one accumulator or
@@ -57,13 +60,14 @@ constexpr int PR = BK / 8;     // packed rows per stage
 constexpr int WPT = 8;         // words per TMEM store (32 columns)
 constexpr int GROUPS = 4;      // dequantisation groups: stage f goes to group f mod 4
 constexpr int SLOTS = 3;       // A slots: stage f goes to slot f mod 3
-constexpr int DQ_WARP0 = 2;    // warps 0, 1: TMA producer, MMA issuer
+constexpr int DQ_WARP0 = 2;    // warps 0, 1: weight producer, MMA issuer
 constexpr int EPI_WARP0 = DQ_WARP0 + 4 * GROUPS;  // four read-out warps
-constexpr int THREADS = (EPI_WARP0 + 4) * 32;
+constexpr int X_WARP = EPI_WARP0 + 4;             // X's producer
+constexpr int THREADS = (X_WARP + 1) * 32;
 constexpr int QW_BYTES = PR * BW * 4;
 constexpr int QW_ROW_BYTES = BW * 4;
 constexpr int S_ROW_BYTES = BW * 2;
-constexpr int kMaxStages = 8;
+constexpr int W_MAX = 10, X_MAX = 8;  // ring stages, at most
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t D_COL = 0;     // two accumulators of up to 32 columns
 constexpr uint32_t D_NEXT = 64;
@@ -76,13 +80,15 @@ static_assert(GROUPS < 2 * SLOTS, "see Bars::aempty");
 static_assert(EPI_WARP0 % 4 == 2 && DQ_WARP0 % 4 == 2, "quarters by warp % 4");
 
 struct Bars {
-  // Use v of ring stage s landed: barrier s + stages * (v & 1).  A group can
+  // Use v of weight stage s landed: barrier s + stages * (v & 1).  A group can
   // come to wait for a load that is not issued yet, with the stage's load
   // before it (another group's, when the ring is no multiple of the groups)
   // still under way: the two parities of one barrier could not tell them apart.
-  uint64_t full[2 * kMaxStages];
-  uint64_t empty[kMaxStages];  // stage read by its group's warps and the MMAs
-  uint64_t afull[SLOTS];       // A slot written (and X permuted) by a group's warps
+  uint64_t wfull[2 * W_MAX];
+  uint64_t wempty[W_MAX];      // stage read by its group's warps
+  uint64_t xfull[X_MAX];       // X stage landed
+  uint64_t xempty[X_MAX];      // MMAs reading it done
+  uint64_t afull[SLOTS];       // A slot written by a group's warps
   // MMAs reading use u of slot a done: barrier a + SLOTS * (u & 1).  A group
   // can come to wait for use u - 1 = stage f - 3 while the MMAs of stage f - 6
   // (use u - 2) still run, which one barrier per slot and its parity could not
@@ -95,22 +101,31 @@ struct Bars {
   int abort_flag;
 };
 
-// Shared memory: the ring, the barriers, the table of token tiles.
+// Shared memory: the rings of X and of the weights, the barriers, the table of
+// token tiles.
 constexpr int kSmemLimit = 227 * 1024 - 1024;
 
 struct Shape {
-  int scale_rows, stage_bytes, stages, smem_bytes;
+  int scale_rows, w_bytes, w_stages, smem_bytes;
 };
+
+// X stages: enough that a stage's X, asked for when the MMAs of the stage that
+// many before are done, lands before its weights are dequantised.
+template <int ROWS>
+constexpr int x_stages() {
+  return ROWS >= 32 ? 5 : ROWS >= 16 ? 6 : 8;
+}
 
 template <int ROWS>
 Shape shape_of(int group_shift, int E) {
   Shape d;
   const int gs = group_shift < 30 ? group_shift : 30;
   d.scale_rows = (BK >> gs) > 1 ? (BK >> gs) : 1;
-  d.stage_bytes = (ROWS * BK * 2 + QW_BYTES + d.scale_rows * S_ROW_BYTES + 1023) & ~1023;
-  const int rest = (int)sizeof(Bars) + ExpertTable<ROWS, ROWS>::bytes(E);
-  d.stages = std::min(kMaxStages, (kSmemLimit - rest) / d.stage_bytes);
-  d.smem_bytes = 1024 + d.stages * d.stage_bytes + rest;
+  d.w_bytes = QW_BYTES + d.scale_rows * S_ROW_BYTES;
+  const int rest =
+      x_stages<ROWS>() * ROWS * BK * 2 + (int)sizeof(Bars) + ExpertTable<ROWS, ROWS>::bytes(E);
+  d.w_stages = std::min(W_MAX, (kSmemLimit - rest) / d.w_bytes);
+  d.smem_bytes = 1024 + d.w_stages * d.w_bytes + rest;
   return d;
 }
 
@@ -119,18 +134,6 @@ Shape shape_of(int group_shift, int E) {
 // shared memory, on which the issuing warps' descriptors depend, would keep
 // those out of the uniform datapath otherwise.
 __device__ __forceinline__ int uniform(int v) { return (int)__reduce_max_sync(0xffffffffu, v); }
-
-// One 16-byte chunk of an X row (eight consecutive k) rewritten in place from
-// natural order to the paired order of the unpacked weights.
-__device__ __forceinline__ void permute_x_chunk(uint8_t* p) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  uint4 o;
-  o.x = prmt(v.x, v.z, 0x5410);
-  o.y = prmt(v.x, v.z, 0x7632);
-  o.z = prmt(v.y, v.w, 0x5410);
-  o.w = prmt(v.y, v.w, 0x7632);
-  *reinterpret_cast<uint4*>(p) = o;
-}
 
 // One stage's 32 words of a thread's column into its 128 TMEM cells of an A
 // slot: eight words at a time, the next eight under way meanwhile.  SMALL: the
@@ -163,9 +166,9 @@ __device__ __forceinline__ bool dequant_stage(const uint8_t* qw, const uint8_t* 
         const uint32_t word = w[c & 1][WPS * g + i];
         uint32_t* out = cells + 4 * (WPS * g + i);
         if (SMALL)
-          dequant_word_paired_small_scale(word, s2, b2, c2, out);
+          dequant_word_natural_small_scale(word, b2, c2, out);
         else
-          dequant_word_paired(word, s2, out);
+          dequant_word_natural(word, s2, out);
       }
     }
     if (c == 0 && !ready()) return false;
@@ -184,23 +187,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                           const __grid_constant__ CUtensorMap qw_map,
                           const __grid_constant__ CUtensorMap s_map, const int32_t* offsets,
                           uint16_t* y, int R, int K, int N, int E, int group_shift, int stages,
-                          int stage_bytes, int scale_rows, int x3d, int* err) {
+                          int w_bytes, int x3d, int* err) {
   constexpr int BT = ROWS < 16 ? 16 : ROWS;  // MMA N
   constexpr int ATOM_BYTES = ROWS * 128;     // X: 64-k atoms of ROWS 128-byte rows
   constexpr int X_BYTES = 4 * ATOM_BYTES;
+  constexpr int XS = x_stages<ROWS>();
   using Table = ExpertTable<ROWS, ROWS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Bars* bar = reinterpret_cast<Bars*>(ring + stages * stage_bytes);
+  uint8_t* w_ring = ring + XS * X_BYTES;
+  Bars* bar = reinterpret_cast<Bars*>(w_ring + stages * w_bytes);
   volatile int* abort_flag = &bar->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gs = min(group_shift, 30);
   const int splits = gridDim.y;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * stages; ++s) mbar_init(&bar->full[s], 1);
-    for (int s = 0; s < stages; ++s)
-      mbar_init(&bar->empty[s], 4 + 1);  // the group's warps + the MMA commit
+    for (int s = 0; s < 2 * stages; ++s) mbar_init(&bar->wfull[s], 1);
+    for (int s = 0; s < stages; ++s) mbar_init(&bar->wempty[s], 4);
+    for (int s = 0; s < XS; ++s) {
+      mbar_init(&bar->xfull[s], 1);
+      mbar_init(&bar->xempty[s], 1);
+    }
     for (int a = 0; a < SLOTS; ++a) mbar_init(&bar->afull[a], 4);
     for (int a = 0; a < 2 * SLOTS; ++a) mbar_init(&bar->aempty[a], 1);
     for (int i = 0; i < 2; ++i) {
@@ -237,37 +245,27 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int n_st = (int)((int64_t)(blockIdx.y + 1) * NS / splits) - st0;
 
   if (warp == 0) {
-    // ---------------- TMA producer (converged; one elected lane issues) ----------------
+    // ---------------- weight producer (converged; one elected lane issues) ----------------
     const int count = uniform(n_items);
     int issued = 0, s = 0, v = 0;  // ring stage, and which use of it
     bool ok = true;
     for (int j = 0; j < count && ok; ++j) {
       const int item = first + j * step;
-      const ExpertTile tt = table.find(item / nblk);
-      const int n0 = (item % nblk) * BW, e = uniform(tt.e), row0 = uniform(tt.row0);
+      const int n0 = (item % nblk) * BW, e = uniform(table.find(item / nblk).e);
       for (int t = 0; t < n_st; ++t) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->empty[s], (uint32_t)(v & 1) ^ 1u,
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->wempty[s], (uint32_t)(v & 1) ^ 1u,
                                                        abort_flag, kWaitLimitNs));
         if (!ok) {
           if (lane == 0) record_timeout(err, bar);
           break;
         }
         if (elect_one()) {
-          uint8_t* st = ring + s * stage_bytes;
-          uint64_t* full = &bar->full[s + stages * (v & 1)];
+          uint8_t* st = w_ring + s * w_bytes;
+          uint64_t* full = &bar->wfull[s + stages * (v & 1)];
           const int k0 = (st0 + t) * BK;
-          // 64-k atoms of X that hold k below K (a 3-D box always fills four)
-          const int atoms = x3d ? 4 : min(4, (K - k0 + 63) / 64);
-          mbar_arrive_expect_tx(full,
-                                QW_BYTES + scale_rows * S_ROW_BYTES + atoms * ATOM_BYTES);
-          tma_load_3d(st + X_BYTES, &qw_map, n0, k0 >> 3, e, full);
-          tma_load_3d(st + X_BYTES + QW_BYTES, &s_map, n0, k0 >> gs, e, full);
-          if (x3d) {
-            tma_load_3d(st, &x_map, 0, row0, k0 >> 6, full);
-          } else {
-            for (int a = 0; a < atoms; ++a)
-              tma_load_2d(st + a * ATOM_BYTES, &x_map, k0 + 64 * a, row0, full);
-          }
+          mbar_arrive_expect_tx(full, w_bytes);
+          tma_load_3d(st, &qw_map, n0, k0 >> 3, e, full);
+          tma_load_3d(st + QW_BYTES, &s_map, n0, k0 >> gs, e, full);
         }
         __syncwarp();
         ++issued;
@@ -281,12 +279,54 @@ __global__ void __launch_bounds__(THREADS, 1)
       // drain: wait (bounded) for the last load issued into each slot
       int never = 0;
       for (int i = issued - 1; i >= 0 && i >= issued - stages; --i)
-        mbar_wait_bounded(&bar->full[i % (2 * stages)], (uint32_t)(i / (2 * stages)) & 1u, &never,
-                          kDrainLimitNs);
+        mbar_wait_bounded(&bar->wfull[i % (2 * stages)], (uint32_t)(i / (2 * stages)) & 1u,
+                          &never, kDrainLimitNs);
     }
     // all copies are issued: the next kernel in the stream may start its
     // prologue (it waits for this grid before touching its inputs)
     if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncwarp();
+  } else if (warp == X_WARP) {
+    // ---------------- X producer (converged; one elected lane issues) ----------------
+    const int count = uniform(n_items);
+    int issued = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int j = 0; j < count && ok; ++j) {
+      const int row0 = uniform(table.find((first + j * step) / nblk).row0);
+      for (int t = 0; t < n_st; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->xempty[s], ph ^ 1u, abort_flag,
+                                                       kWaitLimitNs));
+        if (!ok) {
+          if (lane == 0) record_timeout(err, bar);
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* st = ring + s * X_BYTES;
+          const int k0 = (st0 + t) * BK;
+          // 64-k atoms of X that hold k below K (a 3-D box always fills four)
+          const int atoms = x3d ? 4 : min(4, (K - k0 + 63) / 64);
+          mbar_arrive_expect_tx(&bar->xfull[s], atoms * ATOM_BYTES);
+          if (x3d) {
+            tma_load_3d(st, &x_map, 0, row0, k0 >> 6, &bar->xfull[s]);
+          } else {
+            for (int a = 0; a < atoms; ++a)
+              tma_load_2d(st + a * ATOM_BYTES, &x_map, k0 + 64 * a, row0, &bar->xfull[s]);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == XS) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (*abort_flag) {
+      int never = 0;
+      for (int i = issued - 1; i >= 0 && i >= issued - XS; --i)
+        mbar_wait_bounded(&bar->xfull[i % XS], (uint32_t)(i / XS) & 1u, &never, kDrainLimitNs);
+    }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer (converged; one elected lane issues) ----------------
@@ -295,6 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tm = (uint32_t)uniform((int)tmem);
     bool ok = true;
     int s = 0, a = 0, use = 0;
+    uint32_t xph = 0;
     for (int j = 0; j < count && ok; ++j) {
       const uint32_t d = tm + D_COL + (uint32_t)(j & 1) * D_NEXT;
       if (j >= 2) {
@@ -304,13 +345,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
       }
       for (int t = 0; t < n_st; ++t) {
-        // the stage's X has landed too: its A slot was written from the stage
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag,
-                                          kWaitLimitNs));
+        // both asked at once first: a wait costs 200 cycles even when there is
+        // nothing to wait for
+        const bool there = mbar_test_wait(smem_u32(&bar->xfull[s]), xph) &
+                           mbar_test_wait(smem_u32(&bar->afull[a]), (uint32_t)use & 1u);
+        if (!__all_sync(0xffffffffu, there))
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                              mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag,
+                                                kWaitLimitNs));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * stage_bytes));
+        const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * X_BYTES));
         const uint32_t a_base = tm + A_COL + a * A_SLOT_COLS;
         const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
         const uint32_t keep = t > 0 ? 1u : 0u;
@@ -329,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                          idesc, kk > 0 ? 1u : keep);
           }
           mma_commit(&bar->aempty[a + SLOTS * (use & 1)]);
-          mma_commit(&bar->empty[s]);
+          mma_commit(&bar->xempty[s]);
           if (t == n_st - 1) mma_commit(&bar->dfull[j & 1]);
         }
         __syncwarp();
@@ -337,7 +383,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           a = 0;
           ++use;
         }
-        if (++s == stages) s = 0;
+        if (++s == XS) {
+          s = 0;
+          xph ^= 1u;
+        }
       }
     }
     if (!ok) {
@@ -355,32 +404,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int grp = (warp - DQ_WARP0) >> 2;
     const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
     const int col = 32 * quarter + lane;
-    const int gid = ((warp - DQ_WARP0) & 3) * 32 + lane;
     const uint32_t a_lane = tmem + ((uint32_t)(32 * quarter) << 16) + A_COL;
     const int total = n_items * n_st;
     int s = grp % stages, v = grp / stages;        // ring stage, and which use of it
     int a = grp % SLOTS, use = grp / SLOTS;  // A slot, and which use of it
-    int j = -1, t = grp - GROUPS;  // item, and stage in it
-    int rows = 0;
     bool ok = true;
     for (int f = grp; f < total; f += GROUPS) {
-      t += GROUPS;
-      while (j < 0 || t >= n_st) {
-        if (j >= 0) t -= n_st;
-        ++j;
-        rows = table.find((first + j * step) / nblk).rows;
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->full[s + stages * (v & 1)],
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->wfull[s + stages * (v & 1)],
                                                      (uint32_t)(v >> 1) & 1u, abort_flag,
                                                      kWaitLimitNs));
       if (!ok) break;
-      uint8_t* st = ring + s * stage_bytes;
-      // 32 chunks per row and stage: chunk c of 64-k atom c / 8 (every chunk of
-      // a row is permuted, so the swizzle does not matter)
-      for (int i = gid; i < 32 * rows; i += 128)
-        permute_x_chunk(st + ((i & 31) >> 3) * ATOM_BYTES + (i >> 5) * 128 + (i & 7) * 16);
-      const uint8_t* qw = st + X_BYTES + col * 4;
-      const uint8_t* sc = st + X_BYTES + QW_BYTES + col * 2;
+      const uint8_t* qw = w_ring + s * w_bytes + col * 4;
+      const uint8_t* sc = w_ring + s * w_bytes + QW_BYTES + col * 2;
       // the A slot is free once the MMAs of its previous use have completed
       const auto ready = [&]() -> bool {
         const bool free =
@@ -405,10 +440,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       // qweight and scales of the stage are read (a lane's words were used
       // before it got here)
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->empty[s]);
+      if (lane == 0) mbar_arrive(&bar->wempty[s]);
       if (!ok) break;
       tmem_wait_st();
-      fence_proxy_async_smem();  // the permuted X rows, for the MMAs
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->afull[a]);
@@ -528,8 +562,8 @@ cudaError_t launch_t(const CUtensorMap& x_map, const CUtensorMap& qw_map, const 
   cfg.attrs = attr;
   cfg.numAttrs = splits > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, experts_decode_kernel<WPS, ROWS>, x_map, qw_map, s_map, offsets,
-                            y, (int)R, (int)K, (int)N, (int)E, group_shift, d.stages,
-                            d.stage_bytes, d.scale_rows, x3d, dev.error_word);
+                            y, (int)R, (int)K, (int)N, (int)E, group_shift, d.w_stages,
+                            d.w_bytes, x3d, dev.error_word);
 }
 
 // CTAs that share an item along K: as many as the SMs hold when every item is
@@ -547,7 +581,7 @@ cudaError_t launch_rows(const uint16_t* x, const int32_t* qweight, const uint16_
                       const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
                       int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
   const Shape d = shape_of<ROWS>(group_shift, (int)E);
-  if (d.stages < GROUPS) return cudaErrorInvalidValue;
+  if (d.w_stages < GROUPS) return cudaErrorInvalidValue;
   const int64_t n_groups = (group_shift == 62 || (int64_t(1) << group_shift) >= K)
                                ? 1 : (K + (int64_t(1) << group_shift) - 1) >> group_shift;
   CUtensorMap x_map, qw_map, s_map;
