@@ -132,17 +132,31 @@ __device__ __forceinline__ void dequant_word_paired_small_scale(uint32_t w, uint
   p[3] = hfma2_rn(and_b32(w8, 0x00F000F0u), b2, c2);
 }
 
-// Natural k order for a scale with 0 < s < 2^-4 (b2, c2 from
-// subnormal_form_constants): byte j of the word holds codes k_{2j} (low
-// nibble) and k_{2j+1}; taken from w << 4 and from w, both lie at bits 4..7 of
-// their half, as the subnormals q * 2^-20.  13 operations a word, 17 without.
+// Natural k order, the same idea, for a scale with 0 < s < 2^-5.  Byte j of the
+// word holds codes k_{2j} (low nibble) and k_{2j+1}.  Shifted to bits 3..6 of
+// its byte, a code is the FP16 subnormal q * 2^-21, and the byte's top bit is
+// zero, so that one byte permute can set a pair's low bytes and fill its high
+// bytes with copies of that bit.  12 operations a word; 17 with the
+// magic-number form.
+__device__ __forceinline__ bool scale_fits_natural_form(uint32_t s2) {
+  return (s2 & 0xFFFFu) - 1u < 0x27FFu;  // the low half's bits in 0x0001 .. 0x27FF
+}
+
+__device__ __forceinline__ void natural_form_constants(uint32_t s2, uint32_t& b2, uint32_t& c2) {
+  constexpr uint32_t k1024 = 0x64006400u;     // half2(1024, 1024)
+  constexpr uint32_t k2048 = 0x68006800u;     // half2(2048, 2048)
+  constexpr uint32_t kMinus8 = 0xC800C800u;   // half2(-8, -8)
+  b2 = hmul2_rn(hmul2_rn(s2, k1024), k2048);  // s * 2^21, exact
+  c2 = hmul2_rn(s2, kMinus8);                 // -8 s, exact
+}
+
 __device__ __forceinline__ void dequant_word_natural_small_scale(uint32_t w, uint32_t b2,
                                                                  uint32_t c2, uint32_t n[4]) {
-  const uint32_t w4 = w << 4;
-  n[0] = hfma2_rn(and_b32(prmt(w4, w, 0x4400), 0x00F000F0u), b2, c2);
-  n[1] = hfma2_rn(and_b32(prmt(w4, w, 0x5511), 0x00F000F0u), b2, c2);
-  n[2] = hfma2_rn(and_b32(prmt(w4, w, 0x6622), 0x00F000F0u), b2, c2);
-  n[3] = hfma2_rn(and_b32(prmt(w4, w, 0x7733), 0x00F000F0u), b2, c2);
+  const uint32_t even = and_b32(w << 3, 0x78787878u), odd = and_b32(w >> 1, 0x78787878u);
+  n[0] = hfma2_rn(prmt(even, odd, 0xC480), b2, c2);
+  n[1] = hfma2_rn(prmt(even, odd, 0xD591), b2, c2);
+  n[2] = hfma2_rn(prmt(even, odd, 0xE6A2), b2, c2);
+  n[3] = hfma2_rn(prmt(even, odd, 0xF7B3), b2, c2);
 }
 
 // Same, in natural k order: n[j] = (k_{2j}, k_{2j+1}).

@@ -18,8 +18,8 @@
 //   One wait for the stage, one for the slot and one arrival per 32 words: with
 //   sixteen words per warp between the barriers the waits were a third of all
 //   instructions.
-// * Weights are written in natural k order (13 operations a word for scales
-//   below 2^-4).  The decode kernel's paired order needs 11, and X permuted in
+// * Weights are written in natural k order (12 operations a word for scales
+//   below 2^-5).  The decode kernel's paired order needs 11, and X permuted in
 //   place with a fence for the tensor cores: no faster here.
 // * One elected lane issues the MMAs into one of two accumulators; four warps
 //   of their own read a finished item out and store it while the next one is
@@ -160,7 +160,7 @@ __device__ __forceinline__ bool dequant_stage(const uint8_t* qw, const uint8_t* 
       const uint32_t s2 =
           half2_broadcast(*reinterpret_cast<const uint16_t*>(sc + srow * S_ROW_BYTES));
       uint32_t b2, c2;
-      if (SMALL) subnormal_form_constants(s2, b2, c2);
+      if (SMALL) natural_form_constants(s2, b2, c2);
 #pragma unroll
       for (int i = 0; i < WPS; ++i) {
         const uint32_t word = w[c & 1][WPS * g + i];
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (WPS >= 4) {
 #pragma unroll
         for (int g = 0; g < PR / WPS; ++g)
-          small &= scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
+          small &= scale_fits_natural_form(*reinterpret_cast<const uint16_t*>(
               sc + ((8 * WPS * g) >> gs) * S_ROW_BYTES));  // every load in flight at once
         small = __all_sync(0xffffffffu, small);
       }

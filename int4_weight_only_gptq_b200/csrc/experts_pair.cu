@@ -476,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         small = true;
 #pragma unroll
         for (int r = 0; r < BK / 8; r += WPS)
-          small &= scale_fits_subnormal_form(*reinterpret_cast<const uint16_t*>(
+          small &= scale_fits_natural_form(*reinterpret_cast<const uint16_t*>(
               sc + r / WPS * SC_ROW_BYTES));  // every load in flight at once
         small = __all_sync(0xffffffffu, small);
       }
@@ -519,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 sc + (8 * h + r0) / WPS * SC_ROW_BYTES));
             if (small) {
               uint32_t b2, c2;
-              subnormal_form_constants(s2, b2, c2);
+              natural_form_constants(s2, b2, c2);
 #pragma unroll
               for (int r = r0; r < r0 + PER; ++r)
                 dequant_word_natural_small_scale(w[r], b2, c2, cells + 4 * r);
