@@ -337,7 +337,7 @@ GPTQ_API int gptq_w4a16_gemm_experts(const uint16_t* x_sorted, const int32_t* qw
 /*
  * As gptq_w4a16_gemm_experts, with the kernel forced: kernel_id is one of the
  * GPTQ_KERNEL_* values, tile the most rows of an expert that share one pass
- * over its weights (8, 16 or 32 with GPTQ_KERNEL_DECODE, 0 otherwise; else
+ * over its weights (16 or 32 with GPTQ_KERNEL_DECODE, 0 otherwise; else
  * GPTQ_ERR_KERNEL).  Any choice gives a correct, deterministic result.  Meant
  * for tests and benchmarks that compare the kernels on the same shape.
  */

@@ -571,7 +571,7 @@ def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     x_sorted [R, K] FP16 and offsets [E + 1] int32 as moe_sort returns them,
     qweight [E, K/8, N] int32, scales [E, n_groups, N] FP16.  Rows that belong
     to no expert keep what `out` holds.  kernel and tile force the kernel: tests
-    and benchmarks (KERNEL_DECODE takes a tile of 8, 16 or 32 rows)."""
+    and benchmarks (KERNEL_DECODE takes a tile of 16 or 32 rows)."""
     lib = _lib or load()
     fn = lib.gptq_w4a16_gemm_experts
     if kernel != KERNEL_AUTO or tile != 0:

@@ -241,19 +241,19 @@ int status_of(cudaError_t e) {
 }
 
 // The kernel of the experts' products, and its token tile, from the rows an
-// expert has on average.  Measured (us; tiles of 8 / 16 / 32 on the decode
-// kernel, then the pair kernel) with 64 experts of 2048 x 2048 at 1, 4, 8 and
-// 16 rows: 28 / 28 / 29 / 32, 40 / 36 / 39 / 41, 58 / 45.5 / 45.0 / 46.2 and
-// 86 / 61 / 52 / 47; with 8 experts of 5120 x 17408 at 1, 4, 8 and 16 rows:
-// 69 / 69 / 77 / 84, 95 / 90 / 94 / 109, 127 / 96 / 97 / 109 and 197 / 129 /
-// 101 / 110.
+// expert has on average.  Measured (us; tiles of 16 / 32 on the decode kernel,
+// then the pair kernel) with 64 experts of 2048 x 2048 at 1, 4, 8, 12 and 16
+// rows: 25.8 / 26.8 / 28.7, 32.8 / 34.3 / 36.1, 40.9 / 39.4 / 40.7,
+// 47.4 / 41.6 / 41.2 and 53.4 / 44.7 / 41.5; with 8 experts of 5120 x 17408 at
+// 1, 4, 8, 12 and 16 rows: 66 / 72 / 73, 86 / 90 / 96, 92 / 91 / 96,
+// 105 / 92 / 96 and 118 / 93 / 97.
 int select_experts_kernel(int64_t R, int64_t E, int32_t* tile) {
   const int64_t mean = (R + E - 1) / E;
-  if (mean > 10) {
+  if (mean > 12) {
     *tile = 0;
     return GPTQ_KERNEL_PREFILL;
   }
-  *tile = mean <= 1 ? 8 : mean <= 5 ? 16 : 32;
+  *tile = mean <= 6 ? 16 : 32;
   return GPTQ_KERNEL_DECODE;
 }
 
@@ -266,7 +266,7 @@ int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* sca
   int st = check_shape(R, K, N, group);
   if (st != GPTQ_OK) return st;
   if (kernel_id < GPTQ_KERNEL_AUTO || kernel_id > GPTQ_KERNEL_PREFILL) return GPTQ_ERR_KERNEL;
-  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 8 && tile != 16 && tile != 32 : tile != 0)
+  if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 16 && tile != 32 : tile != 0)
     return GPTQ_ERR_KERNEL;
   if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
   if (!qweight || !scales || !offsets) return GPTQ_ERR_NULL;

@@ -23,11 +23,9 @@
 //   place with a fence for the tensor cores: no faster here.
 // * One elected lane issues the MMAs into one of two accumulators; four warps
 //   of their own read a finished item out and store it while the next one is
-//   multiplied.  (An MMA of 16 tokens takes 15 cycles, into one accumulator or
-//   into four in turn.)  Everything that the descriptors are made of stays
-//   warp-uniform: a branch on the tile's rows inside the issue took the stage's
-//   sixteen MMAs from 310 to over 600 cycles, and its sequence bounds the
-//   kernel as much as the dequantisation does.
+//   multiplied.  An MMA of 16 tokens takes 15 cycles, into one accumulator or
+//   into four in turn; a stage's sixteen with their commits 310 alone, 470
+//   beside warps that keep the issue slots busy.
 // * Few items (splits > 1): the CTAs of a cluster share one item, each taking
 //   a range of K, and add their partial sums in rank order through
 //   distributed shared memory.
@@ -67,7 +65,7 @@ constexpr int THREADS = (X_WARP + 1) * 32;
 constexpr int QW_BYTES = PR * BW * 4;
 constexpr int QW_ROW_BYTES = BW * 4;
 constexpr int S_ROW_BYTES = BW * 2;
-constexpr int W_MAX = 10, X_MAX = 8;  // ring stages, at most
+constexpr int W_MAX = 10, X_MAX = 6;  // ring stages, at most
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t D_COL = 0;     // two accumulators of up to 32 columns
 constexpr uint32_t D_NEXT = 64;
@@ -113,7 +111,7 @@ struct Shape {
 // many before are done, lands before its weights are dequantised.
 template <int ROWS>
 constexpr int x_stages() {
-  return ROWS >= 32 ? 5 : ROWS >= 16 ? 6 : 8;
+  return ROWS >= 32 ? 5 : 6;
 }
 
 template <int ROWS>
@@ -128,12 +126,6 @@ Shape shape_of(int group_shift, int E) {
   d.smem_bytes = 1024 + d.w_stages * d.w_bytes + rest;
   return d;
 }
-
-// A value that every lane of the warp holds, in a form that the compiler knows
-// to be warp-uniform (a warp reduction): loop bounds and addresses read from
-// shared memory, on which the issuing warps' descriptors depend, would keep
-// those out of the uniform datapath otherwise.
-__device__ __forceinline__ int uniform(int v) { return (int)__reduce_max_sync(0xffffffffu, v); }
 
 // One stage's 32 words of a thread's column into its 128 TMEM cells of an A
 // slot: eight words at a time, the next eight under way meanwhile.  SMALL: the
@@ -188,7 +180,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                           const __grid_constant__ CUtensorMap s_map, const int32_t* offsets,
                           uint16_t* y, int R, int K, int N, int E, int group_shift, int stages,
                           int w_bytes, int x3d, int* err) {
-  constexpr int BT = ROWS < 16 ? 16 : ROWS;  // MMA N
   constexpr int ATOM_BYTES = ROWS * 128;     // X: 64-k atoms of ROWS 128-byte rows
   constexpr int X_BYTES = 4 * ATOM_BYTES;
   constexpr int XS = x_stages<ROWS>();
@@ -246,12 +237,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ---------------- weight producer (converged; one elected lane issues) ----------------
-    const int count = uniform(n_items);
     int issued = 0, s = 0, v = 0;  // ring stage, and which use of it
     bool ok = true;
-    for (int j = 0; j < count && ok; ++j) {
+    for (int j = 0; j < n_items && ok; ++j) {
       const int item = first + j * step;
-      const int n0 = (item % nblk) * BW, e = uniform(table.find(item / nblk).e);
+      const int n0 = (item % nblk) * BW, e = table.find(item / nblk).e;
       for (int t = 0; t < n_st; ++t) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->wempty[s], (uint32_t)(v & 1) ^ 1u,
                                                        abort_flag, kWaitLimitNs));
@@ -288,12 +278,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == X_WARP) {
     // ---------------- X producer (converged; one elected lane issues) ----------------
-    const int count = uniform(n_items);
     int issued = 0, s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int j = 0; j < count && ok; ++j) {
-      const int row0 = uniform(table.find((first + j * step) / nblk).row0);
+    for (int j = 0; j < n_items && ok; ++j) {
+      const int row0 = table.find((first + j * step) / nblk).row0;
       for (int t = 0; t < n_st; ++t) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->xempty[s], ph ^ 1u, abort_flag,
                                                        kWaitLimitNs));
@@ -330,14 +319,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer (converged; one elected lane issues) ----------------
-    constexpr uint32_t idesc = idesc_f16_f32(BW, BT);
-    const int count = uniform(n_items);
-    const uint32_t tm = (uint32_t)uniform((int)tmem);
+    constexpr uint32_t idesc = idesc_f16_f32(BW, ROWS);
     bool ok = true;
     int s = 0, a = 0, use = 0;
     uint32_t xph = 0;
-    for (int j = 0; j < count && ok; ++j) {
-      const uint32_t d = tm + D_COL + (uint32_t)(j & 1) * D_NEXT;
+    for (int j = 0; j < n_items && ok; ++j) {
+      const uint32_t d = tmem + D_COL + (uint32_t)(j & 1) * D_NEXT;
       if (j >= 2) {
         ok = __all_sync(0xffffffffu,
                         mbar_wait_bounded(&bar->dempty[j & 1], (uint32_t)((j - 2) >> 1) & 1u,
@@ -357,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * X_BYTES));
-        const uint32_t a_base = tm + A_COL + a * A_SLOT_COLS;
+        const uint32_t a_base = tmem + A_COL + a * A_SLOT_COLS;
         const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
         const uint32_t keep = t > 0 ? 1u : 0u;
         if (elect_one()) {
@@ -623,9 +610,7 @@ cudaError_t launch_experts_decode(const uint16_t* x, const int32_t* qweight,
                                   const uint16_t* scales, const int32_t* offsets, uint16_t* y,
                                   int64_t R, int64_t K, int64_t N, int64_t E, int group_shift,
                                   int tile, cudaStream_t stream, const DeviceInfo& dev) {
-  const auto launch = tile <= 8    ? launch_rows<8>
-                      : tile <= 16 ? launch_rows<16>
-                                   : launch_rows<32>;
+  const auto launch = tile <= 16 ? launch_rows<16> : launch_rows<32>;
   return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
 }
 

@@ -133,7 +133,7 @@ cudaError_t launch_experts_pair(const uint16_t* x, const int32_t* qweight, const
                                 int64_t N, int64_t E, int group_shift, cudaStream_t stream,
                                 const DeviceInfo& dev);
 // The same for few rows per expert (experts_decode.cu): token tiles of at
-// most `tile` (8, 16 or 32) rows.
+// most `tile` (16 or 32) rows.
 cudaError_t launch_experts_decode(const uint16_t* x, const int32_t* qweight,
                                   const uint16_t* scales, const int32_t* offsets, uint16_t* y,
                                   int64_t R, int64_t K, int64_t N, int64_t E, int group_shift,

@@ -99,7 +99,7 @@ def test_experts_argument_checks(lib, name, kw, status):
     assert experts(lib, name, **kw) == status
 
 
-@pytest.mark.parametrize("kernel,tile", [(3, 0), (-1, 0), (1, 0), (1, 64), (2, 16), (0, 16)])
+@pytest.mark.parametrize("kernel,tile", [(3, 0), (-1, 0), (1, 0), (1, 8), (2, 16), (0, 16)])
 def test_experts_kernel_choice_checks(lib, kernel, tile):
     args = [v(a) for a in A[:4]] + [8, 64, 64, 8, 32, v(A[4]), None]
     assert lib.gptq_w4a16_gemm_experts_kernel(*args, kernel, tile) == 9
