@@ -59,6 +59,18 @@ __device__ __forceinline__ int key_of(const Id* ids, int64_t p, int E) {
   return v >= 0 && v < (Id)E ? (int)v : E;
 }
 
+// The lanes whose key equals this lane's: one ballot per bit.  (A warp match
+// instruction takes a time that grows with the number of different keys: with
+// it the places of 65,536 pairs of 128 experts took 23.8 us instead of 12.8.)
+__device__ __forceinline__ unsigned lanes_with_equal(int key, int key_bits) {
+  unsigned same = 0xffffffffu;
+  for (int b = 0; b < key_bits; ++b) {
+    const unsigned set = __ballot_sync(0xffffffffu, (key >> b) & 1);
+    same &= (key >> b) & 1 ? set : ~set;
+  }
+  return same;
+}
+
 // ---- sort, few pairs: one launch ------------------------------------------
 //
 // Every CTA holds all keys in shared memory and counts the places of its own
@@ -159,6 +171,123 @@ __global__ void __launch_bounds__(kSmallThreads, 8)
   }
 }
 
+// ---- sort, more pairs: one launch, every CTA counts all ids --------------------
+//
+// One CTA per SM takes a run of tokens.  It asks for their rows (into L2),
+// reads every id while they arrive, counts the pairs of each expert before its
+// own run and in all, ranks its own pairs, and moves its rows.  Reading all ids
+// on every SM costs less than a launch of its own for the places, while there
+// are few of them and few rows: against the two launches below, in us,
+//   tokens x choices x H   520 x 8 x 2048   4000 x 4 x 512   16000 x 1 x 64
+//     two launches              8.3              8.7              7.8
+//     this one                  5.7              7.3              6.4
+// With more bytes the copy decides, and 32 warps an SM keep less of it in flight
+// than the grid of sort_rows: at 16,384 pairs 42 MB took 12.4 for 13.0, 98 MB
+// 22.4 for 21.6, and 8192 x 2 x 5120 (252 MB) 50 for 44.  Moving the rows by
+// bulk copies through shared memory instead (four warps, up to eight rows each)
+// narrowed that to 48 and cost the small ones half a microsecond.
+constexpr int kSortMidPairs = 16384;
+constexpr int64_t kSortMidBytes = 48 << 20;
+constexpr int kMidThreads = 1024;
+constexpr int kMidWarps = kMidThreads / 32;
+constexpr int kMidIds = 8;    // of a thread at once, all loads in flight
+constexpr int kMidChunks = 4;  // 16-byte chunks of a row per lane
+constexpr int kMidOwn = 256;  // pairs of one CTA: its tokens' choices
+
+template <typename Id>
+__global__ void __launch_bounds__(kMidThreads, 1)
+    sort_mid_kernel(const uint16_t* x, const Id* ids, int M, int H, int topk, int E,
+                    uint16_t* x_sorted, int32_t* offsets, int32_t* dest) {
+  __shared__ int before[GPTQ_MOE_MAX_EXPERTS];  // pairs of the expert before this run
+  __shared__ int total[GPTQ_MOE_MAX_EXPERTS];   // ... in all; then its next place
+  __shared__ int warp_sums[kMidWarps];
+  __shared__ int places[kMidOwn];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = (int)((int64_t)blockIdx.x * M / gridDim.x);
+  const int m1 = (int)((int64_t)(blockIdx.x + 1) * M / gridDim.x);
+  const int P = M * topk, p0 = m0 * topk, p1 = m1 * topk;
+  before[threadIdx.x] = 0;
+  total[threadIdx.x] = 0;
+  wait_previous_grid();
+  let_next_grid_start();
+  {
+    const char* rows = reinterpret_cast<const char*>(x + (int64_t)m0 * H);
+    const int64_t bytes = (int64_t)(m1 - m0) * H * 2;
+    for (int64_t b = 128 * (int64_t)threadIdx.x; b < bytes; b += 128 * kMidThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + b));
+  }
+  __syncthreads();
+  const int key_bits = 32 - __clz(E);  // keys are 0 .. E
+  for (int q = threadIdx.x; q < P; q += kMidIds * kMidThreads) {
+    int key[kMidIds];
+#pragma unroll
+    for (int i = 0; i < kMidIds; ++i)
+      key[i] = q + i * kMidThreads < P ? key_of(ids, q + i * kMidThreads, E) : E;
+#pragma unroll
+    for (int i = 0; i < kMidIds; ++i) {
+      if (key[i] == E) continue;
+      atomicAdd(&total[key[i]], 1);
+      if (q + i * kMidThreads < p0) atomicAdd(&before[key[i]], 1);
+    }
+  }
+  __syncthreads();
+  // thread e: the expert's first row, and this run's first place in it
+  const int all = (int)threadIdx.x < E ? total[threadIdx.x] : 0;
+  int scan = all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) warp_sums[warp] = scan;
+  __syncthreads();
+  int prior = lane < warp ? warp_sums[lane] : 0;  // 32 warps: one lane each
+  prior = __reduce_add_sync(0xffffffffu, prior);
+  const int start = prior + scan - all;
+  if ((int)threadIdx.x < E) {
+    total[threadIdx.x] = start + before[threadIdx.x];
+    if (blockIdx.x == 0) {
+      offsets[threadIdx.x] = start;
+      if ((int)threadIdx.x == E - 1) offsets[E] = start + all;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    for (int p = p0; p < p1; p += 32) {
+      const int k = p + lane < p1 ? key_of(ids, p + lane, E) : E;
+      const unsigned same = lanes_with_equal(k, key_bits);
+      const int lower = __popc(same & ((1u << lane) - 1u));
+      const int at = k < E ? total[k] : 0;
+      __syncwarp();
+      if (k < E && lower == 0) total[k] = at + __popc(same);
+      __syncwarp();
+      if (p + lane < p1) {
+        const int d = k < E ? at + lower : -1;
+        places[p + lane - p0] = d;
+        dest[p + lane] = d;
+      }
+    }
+  }
+  __syncthreads();
+  const int chunks = H / 8, segments = (chunks + 32 * kMidChunks - 1) / (32 * kMidChunks);
+  for (int u = warp; u < (m1 - m0) * segments; u += kMidWarps) {
+    const int mm = u / segments, c0 = (u - mm * segments) * (32 * kMidChunks) + lane;
+    const uint4* src = reinterpret_cast<const uint4*>(x + (int64_t)(m0 + mm) * H);
+    uint4 v[kMidChunks];
+#pragma unroll
+    for (int i = 0; i < kMidChunks; ++i)
+      if (c0 + 32 * i < chunks) v[i] = ld_row_v4(src + c0 + 32 * i);
+    for (int j = 0; j < topk; ++j) {
+      const int d = places[mm * topk + j];
+      if (d < 0) continue;
+      uint4* out = reinterpret_cast<uint4*>(x_sorted + (int64_t)d * H);
+#pragma unroll
+      for (int i = 0; i < kMidChunks; ++i)
+        if (c0 + 32 * i < chunks) out[c0 + 32 * i] = v[i];
+    }
+  }
+}
+
 // ---- sort, many pairs: places by one cluster, then the rows ------------------
 //
 // One cluster of eight CTAs; every warp owns a contiguous run of pairs and
@@ -180,25 +309,12 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t addr) {
   return v;
 }
 
-// Keys of pairs p, p + 32, ..., all loads in flight at once (one by one they
-// cost a memory latency each: 65,536 pairs took 22 us instead of 6).
+// Keys of pairs p, p + 32, ..., all loads in flight at once.
 template <typename Id>
 __device__ __forceinline__ void load_keys(const Id* ids, int64_t p, int64_t end, int E,
                                           int (&key)[kPlaceKeys]) {
 #pragma unroll
   for (int i = 0; i < kPlaceKeys; ++i) key[i] = p + 32 * i < end ? key_of(ids, p + 32 * i, E) : E;
-}
-
-// The lanes whose key equals this lane's: one ballot per bit.  (A warp match
-// instruction takes a time that grows with the number of different keys: with
-// 128 experts it was 15 times slower.)
-__device__ __forceinline__ unsigned lanes_with_equal(int key, int key_bits) {
-  unsigned same = 0xffffffffu;
-  for (int b = 0; b < key_bits; ++b) {
-    const unsigned set = __ballot_sync(0xffffffffu, (key >> b) & 1);
-    same &= (key >> b) & 1 ? set : ~set;
-  }
-  return same;
 }
 
 template <typename Id>
@@ -525,6 +641,13 @@ cudaError_t launch_sort(const uint16_t* x, const Id* ids, int64_t M, int64_t H, 
     const int64_t ctas = std::min<int64_t>(M, 8 * (int64_t)dev.num_sms) + 1;
     const Launch l(ctas, kSmallThreads, (size_t)(P + 3) * sizeof(int), stream);
     return cudaLaunchKernelEx(&l.cfg, sort_small_kernel<Id>, x, ids, (int)M, (int)H, topk, E,
+                              x_sorted, offsets, dest);
+  }
+  const int64_t ctas = std::min<int64_t>(M, dev.num_sms);
+  if (P <= kSortMidPairs && M * H * 2 * (topk + 1) <= kSortMidBytes &&
+      (M + ctas - 1) / ctas * topk <= kMidOwn) {
+    const Launch l(ctas, kMidThreads, 0, stream);
+    return cudaLaunchKernelEx(&l.cfg, sort_mid_kernel<Id>, x, ids, (int)M, (int)H, topk, E,
                               x_sorted, offsets, dest);
   }
   static std::once_flag once[64];

@@ -80,8 +80,14 @@ def within(got, ref, tol, label):
 
 SORT = [  # (tokens, H, topk, E, drop)
     (1, 8, 1, 1, 0.0), (1, 2048, 8, 64, 0.0), (3, 72, 2, 5, 0.3), (37, 1048, 3, 12, 0.1),
-    (512, 264, 8, 128, 0.0),      # as many pairs as one launch takes
-    (513, 264, 8, 128, 0.2),      # one more token: the cluster
+    (512, 264, 8, 128, 0.0),      # as many pairs as the one-launch form for few takes
+    (513, 264, 8, 128, 0.2),      # one more token: every CTA counts all ids
+    (4096, 40, 4, 32, 0.1),       # as many pairs as that takes
+    (4097, 40, 4, 33, 0.1),       # one more token: the cluster
+    # more bytes than it takes, and fewer; each CTA's tokens in one step and more
+    (8192, 1032, 2, 8, 0.5), (2500, 520, 5, 300, 0.3), (5000, 512, 3, 1000, 0.2),
+    (2700, 5120, 2, 8, 0.3), (2100, 8200, 2, 3, 0.1), (1400, 12288, 4, 6, 0.6),
+    (1200, 20000, 4, 5, 0.2), (300, 24584, 16, 20, 0.5), (9000, 1040, 1, 3, 1.0),
     (1500, 1024, 6, 1024, 0.5),   # the most experts
     (4099, 1032, 2, 8, 0.05), (70, 16, 64, 200, 0.0), (300, 40, 33, 100, 0.4),
     (5000, 8, 1, 3, 1.0),         # every pair dropped
