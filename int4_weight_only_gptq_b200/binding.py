@@ -407,12 +407,11 @@ def _device_index(t, name: str) -> int:
 
 
 def _call(fn, index: int, stream, *args):
-    """fn(*args, stream) with the tensors' device current."""
+    """fn(*args, stream) with the tensors' device current; stream: a handle, or
+    None for the current stream."""
     if stream is None:
         # the handle of torch.cuda.current_stream(index), without the object
         stream = torch._C._cuda_getCurrentRawStream(index)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
@@ -420,6 +419,24 @@ def _call(fn, index: int, stream, *args):
             status = fn(*args, stream)
     if status != 0:
         _check(status)
+
+
+def _on_stream(fn, stream, out, *args):
+    """fn(*args) with `stream` current, so that what it allocates is memory of
+    that stream (a block of the caller's stream may still be in use there),
+    kept from reuse until the caller's stream is done with it too.  `out` is
+    the caller's own buffer, if any."""
+    t = args[0]
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+        raise ValueError(f"stream is on {stream.device}, expected {t.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    if caller != stream:
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not out:
+                t.record_stream(caller)
+    return result
 
 
 def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
@@ -432,6 +449,8 @@ def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
     int32): expert e's rows are offsets[e] .. offsets[e + 1] - 1, choice j of
     token m is row dest[m, j] (-1 if dropped), in the order of (m, j) within an
     expert.  The rows from offsets[n_experts] on keep what `out` holds."""
+    if isinstance(stream, torch.cuda.Stream):
+        return _on_stream(moe_sort, stream, out, x, expert_ids, n_experts, out)
     lib = _lib or load()
     dev = _device_index(x, "x")
     if not _fits(x, torch.float16, dev):
@@ -450,7 +469,9 @@ def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
         out = torch.empty((M * topk, H), dtype=torch.float16, device=x.device)
     elif not _fits(out, torch.float16, dev) or out.shape != (M * topk, H):
         _bad(out, "out", torch.float16, dev, (M * topk, H))
-    offsets = x.new_empty(n_experts + 1 if n_experts > 0 else 1, dtype=torch.int32)
+    # (the library refuses any other number of experts)
+    offsets = x.new_empty(n_experts + 1 if 0 < n_experts <= MOE_MAX_EXPERTS else 1,
+                          dtype=torch.int32)
     dest = (torch.empty_like(expert_ids, dtype=torch.int32) if wide
             else torch.empty_like(expert_ids))
     _call(lib.gptq_moe_sort, dev, stream, x.data_ptr(), expert_ids.data_ptr(), 8 if wide else 4,
@@ -464,6 +485,8 @@ def moe_combine(y_sorted: torch.Tensor, dest: torch.Tensor, weights: torch.Tenso
     the order of j, dropped choices (dest -1) left out.  y_sorted [R, H] FP16,
     dest [M, topk] int32 from moe_sort, weights [M, topk] FP32 or None for
     ones (then it is moe_sort's gradient, applied to that of x_sorted)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return _on_stream(moe_combine, stream, out, y_sorted, dest, weights, out)
     lib = _lib or load()
     dev = _device_index(y_sorted, "y_sorted")
     if not _fits(y_sorted, torch.float16, dev):
@@ -492,6 +515,8 @@ def moe_combine_backward(dout: torch.Tensor, y_sorted: torch.Tensor, dest: torch
     dweights [M, topk] FP32) from dout [M, H] FP16.  Rows that no entry of dest
     names keep what `out` (the buffer of dy_sorted) holds; dweights is 0 for
     dropped choices."""
+    if isinstance(stream, torch.cuda.Stream):
+        return _on_stream(moe_combine_backward, stream, out, dout, y_sorted, dest, weights, out)
     lib = _lib or load()
     dev = _device_index(dout, "dout")
     if not _fits(dout, torch.float16, dev):
@@ -572,6 +597,9 @@ def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     qweight [E, K/8, N] int32, scales [E, n_groups, N] FP16.  Rows that belong
     to no expert keep what `out` holds.  kernel and tile force the kernel: tests
     and benchmarks (KERNEL_DECODE takes a tile of 16 or 32 rows)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return _on_stream(gemm_experts, stream, out, x_sorted, qweight, scales, offsets, group,
+                          out, None, kernel, tile)
     lib = _lib or load()
     fn = lib.gptq_w4a16_gemm_experts
     if kernel != KERNEL_AUTO or tile != 0:
@@ -585,8 +613,11 @@ def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torc
     """The gradient of gemm_experts with respect to x_sorted: dx_sorted[r] =
     dy_sorted[r] . dequant(qweight[e], scales[e])^T, [R, K] FP16 from dy_sorted
     [R, N] FP16 (the packed weights are frozen and have no gradient)."""
-    return _experts((_lib or load()).gptq_w4a16_gemm_experts_dx, dy_sorted, qweight, scales, offsets,
-                    group, out, stream, True, "dy_sorted")
+    if isinstance(stream, torch.cuda.Stream):
+        return _on_stream(gemm_experts_dx, stream, out, dy_sorted, qweight, scales, offsets,
+                          group, out)
+    return _experts((_lib or load()).gptq_w4a16_gemm_experts_dx, dy_sorted, qweight, scales,
+                    offsets, group, out, stream, True, "dy_sorted")
 
 
 def dequant(qweight: torch.Tensor, scales: torch.Tensor, group: int,

@@ -47,7 +47,7 @@ struct ExpertTable {
 
   // Called by every thread of the CTA (`threads` of them).  Offsets outside
   // 0 .. R or not ascending are clamped, so that no row outside the tensors
-  // is touched, and reported.
+  // is touched, and reported; the work stays that of R rows.
   __device__ void build(const int32_t* offsets, int R, int threads, int* err) {
     for (int e = threadIdx.x; e < E; e += threads) {
       const int a = offsets[e], b = offsets[e + 1];
@@ -74,7 +74,8 @@ struct ExpertTable {
         if (e < E) tile[e] = before + s - c;
         before += __shfl_sync(0xffffffffu, s, 31);
       }
-      if (threadIdx.x == 0) tile[E] = before;
+      // (offsets that overlap give more tiles than R rows can have)
+      if (threadIdx.x == 0) tile[E] = min(before, min(R, E + R / MAX_N));
     }
     __syncthreads();
   }

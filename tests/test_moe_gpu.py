@@ -613,3 +613,70 @@ def test_abi_takes_the_legacy_default_stream():
     torch.cuda.synchronize()
     a, b, c = B.moe_sort(x, ids, 4)
     assert torch.equal(a, xs) and torch.equal(b, off) and torch.equal(c, dest)
+
+
+def layer_on(stream, x, ids, w, q, s, E, G):
+    """Every operator with stream= and its own outputs."""
+    xs, offsets, dest = B.moe_sort(x, ids, E, stream=stream)
+    y = B.gemm_experts(xs, q, s, offsets, G, stream=stream)
+    out = B.moe_combine(y, dest, w, stream=stream)
+    dy, dw = B.moe_combine_backward(out, y, dest, w, stream=stream)
+    dx = B.gemm_experts_dx(dy, q, s, offsets, G, stream=stream)
+    return xs, offsets, dest, y, out, dy, dw, dx
+
+
+def test_outputs_on_another_stream_take_no_memory_that_the_callers_still_uses():
+    rng = np.random.default_rng(11)
+    M, E, K, N, G = 300, 6, 512, 512, 64
+    q, s = (cu(a) for a in P.make_weights(rng, E, K, N, G))
+    x, ids = cu(P.make_rows(rng, M, K)), cu(P.make_ids(rng, M, E, 2))
+    w = torch.rand((M, 2), device="cuda")
+    want = layer_on(None, x, ids, w, q, s, E, G)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # blocks of these sizes, freed while the caller's stream may still use them
+    freed = [torch.empty_like(t) for t in want for _ in range(3)]
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in freed]
+    del freed
+    got = layer_on(side, x, ids, w, q, s, E, G)
+    for t in got:
+        end = t.data_ptr() + t.numel() * t.element_size()
+        assert all(end <= a or t.data_ptr() >= b for a, b in spans)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    out = torch.empty_like(want[4])
+    assert B.moe_combine(want[3], want[2], w, out=out, stream=side) is out
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[4])
+
+
+def test_captured_on_a_forked_stream():
+    rng = np.random.default_rng(12)
+    M, E, K, N, G = 40, 6, 512, 512, 64
+    q, s = (cu(a) for a in P.make_weights(rng, E, K, N, G))
+    x, ids = cu(P.make_rows(rng, M, K)), cu(P.make_ids(rng, M, E, 2))
+    w = torch.rand((M, 2), device="cuda")
+    want = layer_on(None, x, ids, w, q, s, E, G)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = layer_on(side, x, ids, w, q, s, E, G)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [0, -1, 1025, 10 ** 12])
+def test_sort_refuses_numbers_of_experts(n):
+    x = torch.zeros((4, 64), dtype=torch.float16, device="cuda")
+    with pytest.raises(B.GptqError) as e:
+        B.moe_sort(x, torch.zeros((4, 2), dtype=torch.int32, device="cuda"), n)
+    assert e.value.status == 2  # GPTQ_ERR_SHAPE
