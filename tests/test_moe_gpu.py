@@ -680,3 +680,23 @@ def test_sort_refuses_numbers_of_experts(n):
     with pytest.raises(B.GptqError) as e:
         B.moe_sort(x, torch.zeros((4, 2), dtype=torch.int32, device="cuda"), n)
     assert e.value.status == 2  # GPTQ_ERR_SHAPE
+
+
+@pytest.mark.parametrize("E,R,K,N", [(200, 64, 256, 136), (9, 3000, 2048, 264), (2, 5, 2048, 128)])
+def test_offsets_that_overlap_are_reported(E, R, K, N):
+    rng = np.random.default_rng(E)
+    q, s = (cu(a) for a in P.make_weights(rng, E, K, N, 64))
+    offsets = torch.arange(E + 1, device="cuda", dtype=torch.int32) % 2 * R  # 0, R, 0, R, ...
+    if E == 2:
+        offsets = torch.tensor([0, R, 2], device="cuda", dtype=torch.int32)
+    for gradient in (False, True):
+        rows = cu(P.make_rows(rng, R, N if gradient else K))
+        out = Guarded(R, K if gradient else N)
+        run = B.gemm_experts_dx if gradient else B.gemm_experts
+        good = cu(P.offsets_of([R] + [0] * (E - 1)))
+        want = run(rows, q, s, good, 64)
+        run(rows, q, s, offsets, 64, out=out.t)
+        out.after()
+        assert B.device_error() == ERR_INDEX
+        assert torch.equal(run(rows, q, s, good, 64), want)  # the next call works
+        assert B.device_error() == 0
