@@ -352,7 +352,8 @@ GPTQ_API int gptq_w4a16_gemm_experts_kernel(const uint16_t* x_sorted, const int3
  *   dx_sorted[r] = dy_sorted[r] . dequant(qweight[e], scales[e])^T
  * dy_sorted [R, N] FP16 bits; dx_sorted [R, K] FP16 bits, written in the rows
  * of the experts.  FP32 accumulation, one rounding.  Limits, checks and
- * errors as gptq_w4a16_gemm_experts.
+ * errors as gptq_w4a16_gemm_experts, and N <= GPTQ_MAX_K: the sums run over N,
+ * and longer ones lose accuracy.
  */
 GPTQ_API int gptq_w4a16_gemm_experts_dx(const uint16_t* dy_sorted, const int32_t* qweight,
                                         const uint16_t* scales, const int32_t* offsets,

@@ -612,7 +612,8 @@ def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torc
                     stream=None) -> torch.Tensor:
     """The gradient of gemm_experts with respect to x_sorted: dx_sorted[r] =
     dy_sorted[r] . dequant(qweight[e], scales[e])^T, [R, K] FP16 from dy_sorted
-    [R, N] FP16 (the packed weights are frozen and have no gradient)."""
+    [R, N] FP16 (the packed weights are frozen and have no gradient); N up to
+    65536, the length of the sums."""
     if isinstance(stream, torch.cuda.Stream):
         return _on_stream(gemm_experts_dx, stream, out, dy_sorted, qweight, scales, offsets,
                           group, out)

@@ -269,6 +269,8 @@ int experts_impl(const uint16_t* in, const int32_t* qweight, const uint16_t* sca
   if (kernel_id == GPTQ_KERNEL_DECODE ? tile != 16 && tile != 32 : tile != 0)
     return GPTQ_ERR_KERNEL;
   if (E < 1 || E > GPTQ_MOE_MAX_EXPERTS) return GPTQ_ERR_SHAPE;
+  // the gradient's sums run over N: the limit of K is that of their length
+  if (gradient && N > GPTQ_MAX_K) return GPTQ_ERR_SHAPE;
   if (!qweight || !scales || !offsets) return GPTQ_ERR_NULL;
   if (R == 0) return GPTQ_OK;
   if (!in || !out) return GPTQ_ERR_NULL;

@@ -700,3 +700,18 @@ def test_offsets_that_overlap_are_reported(E, R, K, N):
         assert B.device_error() == ERR_INDEX
         assert torch.equal(run(rows, q, s, good, 64), want)  # the next call works
         assert B.device_error() == 0
+
+
+@pytest.mark.parametrize("counts,tile", [([3, 0, 9], 16), ([3, 0, 30], 32), ([150, 0, 40], 0)])
+@pytest.mark.parametrize("gradient", [False, True], ids=["y", "dx"])
+def test_longest_sums(counts, tile, gradient):
+    if gradient and tile:
+        pytest.skip("the gradient has one kernel")
+    K, N = (72 * 8, 65536) if gradient else (65536, 136)
+    rows, q, s, offsets = product_inputs((counts, K, N, 128, 0), gradient)
+    ref, size = P.product(rows, P.expert_weights(q, s, 128), offsets, gradient)
+    kw = {} if gradient else dict(kernel=B.KERNEL_DECODE if tile else B.KERNEL_PREFILL, tile=tile)
+    run = B.gemm_experts_dx if gradient else B.gemm_experts
+    got = run(cu(rows), cu(q), cu(s), cu(offsets), 128, **kw).cpu().numpy()
+    within(got, ref, P.product_tol(ref, size, 65536), f"{counts} {gradient}")
+    within(got, ref, 1e-2 * (1 + np.abs(ref)), f"{counts} {gradient}, the library's bound")

@@ -181,3 +181,9 @@ def test_plain_forms_agree_with_a_worked_example():
     assert np.array_equal(y[3], rows[3].astype(np.float64) @ w[2].astype(np.float64))
     g, _ = P.product(P.make_rows(rng, 5, 16), w, offsets, gradient=True)
     assert g.shape == (5, 32)
+
+
+def test_experts_gradient_limits_the_length_of_its_sums(lib):
+    assert experts(lib, "gptq_w4a16_gemm_experts_dx", N=65536 + 8, R=0) == SHAPE
+    assert experts(lib, "gptq_w4a16_gemm_experts_dx", N=65536, R=0) == 0
+    assert experts(lib, "gptq_w4a16_gemm_experts", N=65536 + 8, R=0) == 0
