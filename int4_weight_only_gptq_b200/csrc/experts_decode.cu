@@ -318,36 +318,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMA issuer (converged; one elected lane issues) ----------------
-    constexpr uint32_t idesc = idesc_f16_f32(BW, ROWS);
-    bool ok = true;
-    int s = 0, a = 0, use = 0;
-    uint32_t xph = 0;
-    for (int j = 0; j < n_items && ok; ++j) {
-      const uint32_t d = tmem + D_COL + (uint32_t)(j & 1) * D_NEXT;
-      if (j >= 2) {
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&bar->dempty[j & 1], (uint32_t)((j - 2) >> 1) & 1u,
-                                          abort_flag, kWaitLimitNs));
-        if (!ok) break;
-      }
-      for (int t = 0; t < n_st; ++t) {
-        // both asked at once first: a wait costs 200 cycles even when there is
-        // nothing to wait for
-        const bool there = mbar_test_wait(smem_u32(&bar->xfull[s]), xph) &
-                           mbar_test_wait(smem_u32(&bar->afull[a]), (uint32_t)use & 1u);
-        if (!__all_sync(0xffffffffu, there))
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
-                              mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag,
-                                                kWaitLimitNs));
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * X_BYTES));
-        const uint32_t a_base = tmem + A_COL + a * A_SLOT_COLS;
-        const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
-        const uint32_t keep = t > 0 ? 1u : 0u;
-        if (elect_one()) {
+    // ---------------- MMA issuer (one lane does it all) ----------------
+    if (elect_one()) {
+      constexpr uint32_t idesc = idesc_f16_f32(BW, ROWS);
+      bool ok = true;
+      int s = 0, a = 0, use = 0;
+      uint32_t xph = 0;
+      for (int j = 0; j < n_items && ok; ++j) {
+        const uint32_t d = tmem + D_COL + (uint32_t)(j & 1) * D_NEXT;
+        if (j >= 2) {
+          ok = mbar_wait_bounded(&bar->dempty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, abort_flag,
+                                 kWaitLimitNs);
+          if (!ok) break;
+        }
+        for (int t = 0; t < n_st; ++t) {
+          // both asked at once first: a wait costs 200 cycles even when there is
+          // nothing to wait for
+          const bool there = mbar_test_wait(smem_u32(&bar->xfull[s]), xph) &
+                             mbar_test_wait(smem_u32(&bar->afull[a]), (uint32_t)use & 1u);
+          if (!there)
+            ok = mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                 mbar_wait_bounded(&bar->afull[a], (uint32_t)use & 1u, abort_flag, kWaitLimitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t x_desc = smem_desc_sw128(smem_u32(ring + s * X_BYTES));
+          const uint32_t a_base = tmem + A_COL + a * A_SLOT_COLS;
+          const int nk = min(BK, K - (st0 + t) * BK) / 16;  // k16 steps below K
+          const uint32_t keep = t > 0 ? 1u : 0u;
           if (nk == BK / 16) {
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
@@ -364,26 +361,24 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_commit(&bar->aempty[a + SLOTS * (use & 1)]);
           mma_commit(&bar->xempty[s]);
           if (t == n_st - 1) mma_commit(&bar->dfull[j & 1]);
-        }
-        __syncwarp();
-        if (++a == SLOTS) {
-          a = 0;
-          ++use;
-        }
-        if (++s == XS) {
-          s = 0;
-          xph ^= 1u;
+          if (++a == SLOTS) {
+            a = 0;
+            ++use;
+          }
+          if (++s == XS) {
+            s = 0;
+            xph ^= 1u;
+          }
         }
       }
-    }
-    if (!ok) {
-      if (lane == 0) record_timeout(err, bar);
-      // wait (bounded) for the MMAs already issued before TMEM is freed
-      uint64_t* last = &bar->aempty[a + SLOTS * (use & 1)];
-      if (elect_one()) mma_commit(last);
-      __syncwarp();
-      int never = 0;
-      mbar_wait_bounded(last, (uint32_t)(use >> 1) & 1u, &never, kDrainLimitNs);
+      if (!ok) {
+        record_timeout(err, bar);
+        // wait (bounded) for the MMAs already issued before TMEM is freed
+        uint64_t* last = &bar->aempty[a + SLOTS * (use & 1)];
+        mma_commit(last);
+        int never = 0;
+        mbar_wait_bounded(last, (uint32_t)(use >> 1) & 1u, &never, kDrainLimitNs);
+      }
     }
     __syncwarp();
   } else if (warp < EPI_WARP0) {

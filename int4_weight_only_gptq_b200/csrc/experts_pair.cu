@@ -345,10 +345,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int i = issued - 1; i >= 0 && i >= issued - ring; --i)
         mbar_wait_bounded(&full[i % ring], (uint32_t)(i / ring) & 1u, &never, kDrainLimitNs);
     }
+    // all copies are issued: the next kernel in the stream may start its
+    // prologue (it waits for this grid before touching its inputs)
+    if (warp == 2 && lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncwarp();  // the whole warp reaches the cluster barrier below together
   } else if (warp == 1) {
-    // ---------------- pair MMA issuer (even CTA) ----------------
-    if (even) {
+    // ---------------- pair MMA issuer (even CTA; one lane does it all) ----------------
+    if (even && elect_one()) {
       bool ok = true;
       int it = 0, s = 0, a = 0, last_n = 0;
       uint32_t xph = 0, aph = 0;
@@ -361,13 +364,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // the tile before the last has been read out; the last one too, where
         // the two share accumulator columns
         if (it > 1)
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar->dempty[it & 1], (uint32_t)((it - 2) >> 1) & 1u,
-                                            abort_flag, kWaitLimitNs));
+          ok = mbar_wait_bounded(&bar->dempty[it & 1], (uint32_t)((it - 2) >> 1) & 1u, abort_flag,
+                                 kWaitLimitNs);
         if (ok && it > 0 && max(n, last_n) > (int)D_HALF)
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bar->dempty[(it - 1) & 1],
-                                                         (uint32_t)((it - 1) >> 1) & 1u,
-                                                         abort_flag, kWaitLimitNs));
+          ok = mbar_wait_bounded(&bar->dempty[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u,
+                                 abort_flag, kWaitLimitNs);
         if (!ok) break;
         tc_fence_after();
         last_n = n;
@@ -379,43 +380,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           bool there = mbar_test_wait(smem_u32(&bar->xfull[s]), xph) &
                        mbar_test_wait(smem_u32(&bar->afull[a]), aph);
           if (H == 2) there &= mbar_test_wait(smem_u32(&bar->afull[a + H - 1]), aph);
-          if (!__all_sync(0xffffffffu, there))
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
-                                mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
-                                (H == 1 || mbar_wait_bounded(&bar->afull[a + H - 1], aph,
-                                                             abort_flag, kWaitLimitNs)));
+          if (!there)
+            ok = mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
+                 mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
+                 (H == 1 || mbar_wait_bounded(&bar->afull[a + H - 1], aph, abort_flag,
+                                              kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-              const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES)) +
-                                    (uint64_t)((2 * h * atom_bytes) >> 4);
-              const uint64_t b_hi = b_lo + (uint64_t)(atom_bytes >> 4);
-              const uint32_t a_base = tmem + A_COL + (a + h) * A_STAGE_COLS;
-              // k16 steps that hold columns below C
-              const int nk = min(BK, C - kb * KST - h * BK + 15) / 16;
-              const uint32_t keep = kb > 0 || h > 0 ? 1u : 0u;
-              if (nk == BK / 16) {
+          for (int h = 0; h < H; ++h) {
+            const uint64_t b_lo = smem_desc_sw128(smem_u32(xs + s * X_STAGE_BYTES)) +
+                                  (uint64_t)((2 * h * atom_bytes) >> 4);
+            const uint64_t b_hi = b_lo + (uint64_t)(atom_bytes >> 4);
+            const uint32_t a_base = tmem + A_COL + (a + h) * A_STAGE_COLS;
+            // k16 steps that hold columns below C
+            const int nk = min(BK, C - kb * KST - h * BK + 15) / 16;
+            const uint32_t keep = kb > 0 || h > 0 ? 1u : 0u;
+            if (nk == BK / 16) {
 #pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk)
-                  mma_f16_ts_pair(d, a_base + kk * 8,
-                                  (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4),
-                                  idesc, kk > 0 ? 1u : keep);
-              } else {
+              for (int kk = 0; kk < BK / 16; ++kk)
+                mma_f16_ts_pair(d, a_base + kk * 8,
+                                (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
+                                kk > 0 ? 1u : keep);
+            } else {
 #pragma unroll 1
-                for (int kk = 0; kk < nk; ++kk)
-                  mma_f16_ts_pair(d, a_base + kk * 8,
-                                  (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4),
-                                  idesc, kk > 0 ? 1u : keep);
-              }
-              mma_commit_pair(&bar->aempty[a + h], kPairMask);
+              for (int kk = 0; kk < nk; ++kk)
+                mma_f16_ts_pair(d, a_base + kk * 8,
+                                (kk < 4 ? b_lo : b_hi) + (uint64_t)(((kk & 3) * 32) >> 4), idesc,
+                                kk > 0 ? 1u : keep);
             }
-            mma_commit_pair(&bar->xempty[s], kPairMask);
-            if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
+            mma_commit_pair(&bar->aempty[a + h], kPairMask);
           }
-          __syncwarp();
+          mma_commit_pair(&bar->xempty[s], kPairMask);
+          if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
           if (++s == XS) {
             s = 0;
             xph ^= 1u;
@@ -428,10 +425,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) {
-        if (lane == 0) record_timeout(err, bar);
+        record_timeout(err, bar);
         // wait for the MMAs already issued before anyone frees TMEM
-        if (elect_one()) mma_commit_pair(&bar->aempty[a + H - 1], kPairMask);
-        __syncwarp();
+        mma_commit_pair(&bar->aempty[a + H - 1], kPairMask);
         int never = 0;
         mbar_wait_bounded(&bar->aempty[a + H - 1], aph, &never, kDrainLimitNs);
       }
