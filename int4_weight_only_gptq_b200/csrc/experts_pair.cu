@@ -15,10 +15,11 @@
 // * A tile holds up to BT = 128 or 256 rows of one expert; the MMA's width is
 //   the rows rounded up to 32, so an expert with few rows pays for those only.
 //   The copy box of X has half as many rows per CTA (a tensor map for each
-//   width): up to 128 tokens, L2 reads of X are what bounds the kernel.  Rows
-//   that a box reads past the tile belong to other experts (or
-//   read as zero past the tensor): each is a column of the accumulator of its
-//   own, which is never stored.
+//   width), so that a tile reads no more of X from L2 than it multiplies: with
+//   128 rows per expert all column pairs together read 9.7 TB/s.  Rows that a
+//   box reads past the tile belong to other experts (or read as zero past the
+//   tensor): each is a column of the accumulator of its own, which is never
+//   stored.
 // * Four warps of their own read a finished accumulator out.  Tiles of up to
 //   128 rows alternate between the two halves of the accumulator columns, so
 //   the next tile's MMAs run meanwhile: with few rows per expert a tile takes
@@ -67,11 +68,17 @@ constexpr int BK = 128;   // contraction per A slot (eight k16 MMAs)
 constexpr int XS = 3;     // X ring stages
 constexpr int WS_MAX = 8;  // weight-tile ring stages (qweight + scales), at most
 constexpr int AS = 4;     // A slots in TMEM (BK each)
+constexpr int FS = 4;     // barriers of ready stages
 constexpr int DQ_GROUPS = 4;             // dequantisation groups: group g takes slots' worth g mod 4
 constexpr int DQ_WARPS = 4 * DQ_GROUPS;  // one warp per TMEM lane quarter in each group
-constexpr int DQ_WARP0 = 3;  // warps 0, 1, 2: X producer, MMA issuer, weight producer
-constexpr int EPI_WARP0 = DQ_WARP0 + DQ_WARPS;  // four read-out warps
-constexpr int THREADS = (EPI_WARP0 + 4) * 32;
+// Warps: dequantisation from 0, four for the read-out, the producers, the MMA
+// issuer.  In that order: beside warps of arithmetic alone, a warp behind them
+// got to issue twice as often as one before them (a loop of 16 MMAs and their
+// commits took 1860 cycles there, 4230 as warp 0).  Here that gives 1 % with 32
+// rows per expert (42.3 -> 41.8 us, 64 experts of 2048 x 2048).
+constexpr int EPI_WARP0 = DQ_WARPS;
+constexpr int X_WARP = EPI_WARP0 + 4, W_WARP = X_WARP + 1, MMA_WARP = W_WARP + 1;
+constexpr int THREADS = (MMA_WARP + 1) * 32;
 constexpr int S_ROW_BYTES = BW * 2;                // a scale row of 128 columns: 256 B
 constexpr int X_STAGE_BYTES = 32 * 1024;           // 128 rows x 128 or 64 rows x 256 columns
 constexpr int W_RING_BYTES = 80 * 1024;
@@ -113,14 +120,17 @@ struct Geo {
 static_assert(1024 + TABLE_OFF + ExpertTable<256, 32>::bytes(GPTQ_MOE_MAX_EXPERTS) <= 227 * 1024,
               "shared memory per CTA");
 
-// Both CTAs hold the full set; xfull, afull and dempty are only used in the
-// even CTA.  dfull and dempty of tile i: entry i mod 2.
+// Both CTAs hold the full set; full and dempty are only used in the even CTA.
+// dfull and dempty of tile i: entry i mod 2.
 struct PairBarriers {
-  uint64_t xfull[XS];   // both halves of the X stage landed (even CTA)
+  // Stage f is ready, entry f mod 4: both halves of X landed, and the group
+  // warps of both CTAs wrote its A slots: one barrier for the MMA lane to ask.
+  // (Nobody signals stage f before stage f - 4 is done: X waits for
+  // f - 3, an A slot for its last use, two or four stages before.)
+  uint64_t full[FS];
   uint64_t xempty[XS];  // pair MMAs reading the X stage done
   uint64_t wfull[WS_MAX];   // this CTA's qweight and scale tiles landed
   uint64_t wempty[WS_MAX];  // weight tiles read by this CTA's group warps
-  uint64_t afull[AS];   // A slot written by the group warps of both CTAs (even CTA)
   uint64_t aempty[AS];  // pair MMAs reading the A slot done
   uint64_t dfull[2];    // all MMAs of the tile done
   uint64_t dempty[2];   // accumulator read out by both CTAs' read-out warps (even CTA)
@@ -216,7 +226,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < XS; ++s) {
-      mbar_init(&bar->xfull[s], 1);   // the even CTA's expect_tx; bytes from both CTAs
       mbar_init(&bar->xempty[s], 1);  // one pair commit
     }
     for (int j = 0; j < WS; ++j) {
@@ -224,9 +233,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&bar->wempty[j], 4 * H);  // the four warps of each of its groups
     }
     for (int j = 0; j < AS; ++j) {
-      mbar_init(&bar->afull[j], 2 * 4);   // the slot's group warps in both CTAs
       mbar_init(&bar->aempty[j], 1);      // one pair commit
     }
+    // the even CTA's expect_tx (bytes from both CTAs), and the group warps of
+    // the stage's slots in both
+    for (int f = 0; f < FS; ++f) mbar_init(&bar->full[f], 1 + 2 * 4 * H);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar->dfull[i], 1);       // one pair commit per tile
       mbar_init(&bar->dempty[i], 2 * 4);  // the read-out warps of both CTAs
@@ -234,17 +245,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bar->abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == X_WARP && lane == 0) {
     for (int i = 0; i < BT / 32; ++i) prefetch_tensormap(&x_maps.width[i]);
     prefetch_tensormap(&qw_map);
     prefetch_tensormap(&s_map);
     prefetch_tensormap(&y_map);
   }
   __syncwarp();
-  if (warp == 1) {
+  if (warp == MMA_WARP) {
     tmem_alloc_pair(&bar->tmem_base, TMEM_COLS);
     tmem_relinquish_pair();
   }
+  // both CTAs' barriers are initialised and TMEM is allocated before any thread
+  // signals the other CTA: this one says so now, and asks for the other's word
+  // once its table is built
+  tc_fence_before();
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // the offsets and X may come from the previous kernel of the stream
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Walk<typename G_::Table> walk;
@@ -259,27 +276,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int NT = walk.count();          // tiles of this cluster
   const int KB = (C + KST - 1) / KST;   // stages per tile
   const int G = NT * KB;                // stages of this cluster, over all its tiles
-  // the list is complete; both CTAs' barriers are initialised and TMEM is
-  // allocated before any thread signals the other CTA
-  tc_fence_before();
-  cluster_sync_all();
+  __syncthreads();  // the list is complete
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   // the even CTA's barriers that both CTAs signal
-  const uint32_t xfull_even = map_to_rank(smem_u32(&bar->xfull[0]), 0);
-  const uint32_t afull_even = map_to_rank(smem_u32(&bar->afull[0]), 0);
+  const uint32_t full_even = map_to_rank(smem_u32(&bar->full[0]), 0);
   const uint32_t dempty_even = map_to_rank(smem_u32(&bar->dempty[0]), 0);
 
-  if (warp == 0 || warp == 2) {
-    // ---------------- TMA producers: X half (warp 0), weights (warp 2) ----------------
+  if (warp == X_WARP || warp == W_WARP) {
+    // ---------------- TMA producers: X half, weights ----------------
     // Converged warps; one elected lane issues.
     int kb = 0, it = 0, o0 = 0, s = 0, issued = 0;
     uint32_t ph = 0;
     ExpertTile tt{0, 0, 0, 32};
     if (NT > 0) tt = walk.at(0, rank, o0);
     bool ok = true;
-    uint64_t* const empty = warp == 0 ? bar->xempty : bar->wempty;
-    const int ring = warp == 0 ? XS : WS;
+    uint64_t* const empty = warp == X_WARP ? bar->xempty : bar->wempty;
+    const int ring = warp == X_WARP ? XS : WS;
     for (int g = 0; g < G; ++g) {
       ok = __all_sync(0xffffffffu,
                       mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, kWaitLimitNs));
@@ -288,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         break;
       }
       const int c0 = kb * KST;
-      if (warp == 0) {
+      if (warp == X_WARP) {
         // The odd CTA's half of the token tile may lie wholly past the last
         // row of X: then it loads nothing and the even CTA expects only its
         // own bytes; the MMA reads stale shared memory for token columns that
@@ -298,12 +312,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const bool odd_rows = tt.row0 + tt.n / 2 < R;
         if (elect_one()) {
           uint8_t* dst = xs + s * X_STAGE_BYTES;
-          const uint32_t bar_c = xfull_even + 8u * (uint32_t)s;
+          const uint32_t bar_c = full_even + 8u * (uint32_t)(g % FS);
           const uint32_t atom_bytes = tt.n / 2 * 128;
           // atoms that hold columns below C (a 3-D box always fills all)
           const int atoms = x3d ? G_::ATOMS : min(G_::ATOMS, (C - c0 + 63) / 64);
           if (even)
-            mbar_arrive_expect_tx(&bar->xfull[s], (odd_rows ? 2u : 1u) * atoms * atom_bytes);
+            mbar_arrive_expect_tx(&bar->full[g % FS], (odd_rows ? 2u : 1u) * atoms * atom_bytes);
           if (even || odd_rows) {
             if (x3d) {
               tma_load_3d_pair(dst, x_map, 0, row, c0 / 64, bar_c);
@@ -337,24 +351,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (++it < NT) tt = walk.at(it, rank, o0);
       }
     }
-    if (*abort_flag && (even || warp == 2)) {
+    if (*abort_flag && (even || warp == W_WARP)) {
       // drain: wait for the last loads issued into each slot (the odd CTA's X
-      // loads complete on the even CTA's barriers, which the even CTA drains)
+      // loads complete on the even CTA's barriers, which the even CTA drains;
+      // where a stage's A slots are never written, the limit is that wait)
       int never = 0;
-      uint64_t* const full = warp == 0 ? bar->xfull : bar->wfull;
+      uint64_t* const full = warp == X_WARP ? bar->full : bar->wfull;
+      const int entries = warp == X_WARP ? FS : ring;
       for (int i = issued - 1; i >= 0 && i >= issued - ring; --i)
-        mbar_wait_bounded(&full[i % ring], (uint32_t)(i / ring) & 1u, &never, kDrainLimitNs);
+        mbar_wait_bounded(&full[i % entries], (uint32_t)(i / entries) & 1u, &never,
+                          kDrainLimitNs);
     }
     // all copies are issued: the next kernel in the stream may start its
     // prologue (it waits for this grid before touching its inputs)
-    if (warp == 2 && lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == W_WARP && lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncwarp();  // the whole warp reaches the cluster barrier below together
-  } else if (warp == 1) {
+  } else if (warp == MMA_WARP) {
     // ---------------- pair MMA issuer (even CTA; one lane does it all) ----------------
     if (even && elect_one()) {
       bool ok = true;
-      int it = 0, s = 0, a = 0, last_n = 0;
-      uint32_t xph = 0, aph = 0;
+      int it = 0, f = 0, s = 0, a = 0, last_n = 0;  // tile; stage, its X stage and A slot
       for (; it < NT && ok; ++it) {
         int o0;
         const int n = walk.at(it, rank, o0).n;
@@ -374,17 +390,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         last_n = n;
         for (int kb = 0; kb < KB; ++kb) {
           // the stage's A slots: a, and with two per stage a + 1 (a is even then)
-          // All of them are asked at once first: waits that have nothing to wait
-          // for, one after the other, cost 200 cycles each under load, half the
-          // time of a small tile's stage.
-          bool there = mbar_test_wait(smem_u32(&bar->xfull[s]), xph) &
-                       mbar_test_wait(smem_u32(&bar->afull[a]), aph);
-          if (H == 2) there &= mbar_test_wait(smem_u32(&bar->afull[a + H - 1]), aph);
-          if (!there)
-            ok = mbar_wait_bounded(&bar->xfull[s], xph, abort_flag, kWaitLimitNs) &&
-                 mbar_wait_bounded(&bar->afull[a], aph, abort_flag, kWaitLimitNs) &&
-                 (H == 1 || mbar_wait_bounded(&bar->afull[a + H - 1], aph, abort_flag,
-                                              kWaitLimitNs));
+          ok = mbar_wait_bounded(&bar->full[f % FS], (uint32_t)(f / FS) & 1u, abort_flag,
+                                 kWaitLimitNs);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -413,15 +420,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           mma_commit_pair(&bar->xempty[s], kPairMask);
           if (kb == KB - 1) mma_commit_pair(&bar->dfull[it & 1], kPairMask);  // tile done
-          if (++s == XS) {
-            s = 0;
-            xph ^= 1u;
-          }
-          a += H;
-          if (a == AS) {
-            a = 0;
-            aph ^= 1u;
-          }
+          ++f;
+          if (++s == XS) s = 0;
+          a = (a + H) % AS;
         }
       }
       if (!ok) {
@@ -429,14 +430,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // wait for the MMAs already issued before anyone frees TMEM
         mma_commit_pair(&bar->aempty[a + H - 1], kPairMask);
         int never = 0;
-        mbar_wait_bounded(&bar->aempty[a + H - 1], aph, &never, kDrainLimitNs);
+        mbar_wait_bounded(&bar->aempty[a + H - 1], (uint32_t)(f * H / AS) & 1u, &never,
+                          kDrainLimitNs);
       }
     }
     __syncwarp();  // the whole warp reaches the cluster barrier below together
   } else if (warp < EPI_WARP0) {
     // ---------------- dequantisation ----------------
     const int quarter = warp & 3;            // TMEM lanes 32*quarter .. +31
-    const int j = (warp - DQ_WARP0) >> 2;    // group: slots' worth f = j mod 4, A slot j
+    const int j = warp >> 2;    // group: slots' worth f = j mod 4, A slot j
     const uint32_t a_slot =
         tmem + ((uint32_t)(32 * quarter) << 16) + A_COL + j * A_STAGE_COLS;
     // forward: this thread's column in weight slot 0; gradient: its packed
@@ -458,8 +460,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t pick_hi = half ? 0x7733u : 0x5511u;  // second byte
 
     bool ok = true;
-    int jw = j / H;              // weight stage's slot and its phase
-    uint32_t pw = 0, ph = 0;     // ... and the A slot's
+    int jw = j / H, f = j / H;   // weight stage's slot, the stage
+    uint32_t pw = 0, ph = 0;     // phases of the weight slot and the A slot
     for (int g = j; g < G * H; g += DQ_GROUPS) {
       const uint8_t* qw = qw0 + jw * W_STAGE_BYTES;
       const uint8_t* sc = sc0 + jw * W_STAGE_BYTES;
@@ -546,7 +548,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tmem_wait_st();  // the whole warp's cells are in TMEM
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(afull_even + 8u * (uint32_t)j);
+      if (lane == 0) mbar_arrive_cluster(full_even + 8u * (uint32_t)(f % FS));
+      f += DQ_GROUPS / H;
       ph ^= 1u;
       jw += DQ_GROUPS / H;
       if (jw >= WS) {
@@ -646,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
-  if (warp == 1) {
+  if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);
   }
