@@ -242,11 +242,11 @@ int status_of(cudaError_t e) {
 
 // The kernel of the experts' products, and its token tile, from the rows an
 // expert has on average.  Measured (us; tiles of 16 / 32 on the decode kernel,
-// then the pair kernel) with 64 experts of 2048 x 2048 at 1, 4, 8, 12 and 16
-// rows: 25.8 / 26.8 / 28.7, 32.8 / 34.3 / 36.1, 40.9 / 39.4 / 40.7,
-// 47.4 / 41.6 / 41.2 and 53.4 / 44.7 / 41.5; with 8 experts of 5120 x 17408 at
-// 1, 4, 8, 12 and 16 rows: 66 / 72 / 73, 86 / 90 / 96, 92 / 91 / 96,
-// 105 / 92 / 96 and 118 / 93 / 97.
+// then the pair kernel) at 1, 4, 6, 8, 12 and 16 rows: with 64 experts of 2048 x
+// 2048 25.6 / 26.3 / 26.9, 32.4 / 33.8 / 34.0, 38.0 / 37.4 / 38.4, 40.6 / 38.4 /
+// 38.7, 46.5 / 41.0 / 39.4 and 52.3 / 43.7 / 39.3; with 8 experts of 5120 x 17408
+// 65 / 69 / 70, 85 / 87 / 91, 85 / 88 / 92, 90 / 89 / 92, 103 / 89 / 93 and
+// 115 / 90 / 93.
 int select_experts_kernel(int64_t R, int64_t E, int32_t* tile) {
   const int64_t mean = (R + E - 1) / E;
   if (mean > 12) {

@@ -732,17 +732,21 @@ cudaError_t launch_bt(const uint16_t* x, const int32_t* qweight, const uint16_t*
 }
 
 // The token tile.  256 tokens move half the weights per product, 128 waste
-// less on ragged row counts and give more tiles.  Measured with 64 experts of
-// 2048 x 2048, rows per expert on average 64 / 128 / 256 / 512: 56 / 80 / 131 /
-// 239 us with 128 tokens, 69 / 87 / 133 / 236 us with 256; with 8 experts of
-// 5120 x 17408, 128 / 256 / 512: 194 / 317 / 593 us against 187 / 300 / 543 us.
+// less on ragged row counts, give more tiles and overlap their read-out.  In us
+// with 128 / 256 tokens, by rows per expert on average:
+//   64 experts of 2048 x 2048, 64: 50 / 65, 128: 72 / 83, 256: 120 / 128,
+//     512: 223 / 230 (the gradient 128: 75 / 84, 256: 125 / 130)
+//   8 experts of 5120 x 17408, 64: 116 / 146, 128: 176 / 180, 256: 292 / 292,
+//     512: 541 / 528
+//   the gradient of 8 experts of 17408 x 5120, under sustained load, 192:
+//     288 / 284, 256: 354 / 350, 384: 498 / 474, 512: 656 / 622
 template <bool DX, int WPS>
 cudaError_t launch_pair(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
                         const int32_t* offsets, uint16_t* y, int64_t R, int64_t K, int64_t N,
                         int64_t E, int group_shift, cudaStream_t stream, const DeviceInfo& dev) {
   const int64_t n_pairs = ((DX ? K : N) + 2 * BW - 1) / (2 * BW);
   const bool few = (E + R / 256) * n_pairs < dev.num_sms / 2;  // not a tile for each cluster
-  const auto launch = R <= 160 * E || few ? launch_bt<DX, 128, WPS> : launch_bt<DX, 256, WPS>;
+  const auto launch = R <= 256 * E || few ? launch_bt<DX, 128, WPS> : launch_bt<DX, 256, WPS>;
   return launch(x, qweight, scales, offsets, y, R, K, N, E, group_shift, stream, dev);
 }
 

@@ -702,11 +702,10 @@ def test_offsets_that_overlap_are_reported(E, R, K, N):
         assert B.device_error() == 0
 
 
-@pytest.mark.parametrize("counts,tile", [([3, 0, 9], 16), ([3, 0, 30], 32), ([150, 0, 40], 0)])
-@pytest.mark.parametrize("gradient", [False, True], ids=["y", "dx"])
+@pytest.mark.parametrize("counts,tile,gradient", [
+    ([3, 0, 9], 16, False), ([3, 0, 30], 32, False), ([150, 0, 40], 0, False),
+    ([150, 0, 40], 0, True)])
 def test_longest_sums(counts, tile, gradient):
-    if gradient and tile:
-        pytest.skip("the gradient has one kernel")
     K, N = (72 * 8, 65536) if gradient else (65536, 136)
     rows, q, s, offsets = product_inputs((counts, K, N, 128, 0), gradient)
     ref, size = P.product(rows, P.expert_weights(q, s, 128), offsets, gradient)
@@ -715,3 +714,17 @@ def test_longest_sums(counts, tile, gradient):
     got = run(cu(rows), cu(q), cu(s), cu(offsets), 128, **kw).cpu().numpy()
     within(got, ref, P.product_tol(ref, size, 65536), f"{counts} {gradient}")
     within(got, ref, 1e-2 * (1 + np.abs(ref)), f"{counts} {gradient}, the library's bound")
+
+
+@pytest.mark.parametrize("G", [16, 32, 64, 128, -1])
+@pytest.mark.parametrize("gradient", [False, True], ids=["y", "dx"])
+def test_product_of_many_rows(G, gradient):
+    """Enough rows and columns for the tiles of 256 rows."""
+    K, N = (5136, 200) if gradient else (208, 5128)
+    rows, q, s, offsets = product_inputs(([700, 0, 333], K, N, G, 0), gradient)
+    ref, size = P.product(rows, P.expert_weights(q, s, G), offsets, gradient)
+    out = Guarded(1033, K if gradient else N, seed=5)
+    run = B.gemm_experts_dx if gradient else B.gemm_experts
+    run(cu(rows), cu(q), cu(s), cu(offsets), G, out=out.t)
+    within(out.after(), ref, P.product_tol(ref, size, N if gradient else K),
+           f"{'dx' if gradient else 'y'} K={K} N={N} G={G}")
