@@ -241,9 +241,22 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// The .aligned forms want a warp's threads to execute them together: the warp
+// barrier sees to it after branches and loops that they leave one by one (no
+// cost measured).
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Barrier among `count` threads (whole warps) of this CTA on named barrier

@@ -260,8 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // signals the other CTA: this one says so now, and asks for the other's word
   // once its table is built
   tc_fence_before();
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  cluster_arrive();
   // the offsets and X may come from the previous kernel of the stream
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Walk<typename G_::Table> walk;
@@ -277,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int KB = (C + KST - 1) / KST;   // stages per tile
   const int G = NT * KB;                // stages of this cluster, over all its tiles
   __syncthreads();  // the list is complete
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   // the even CTA's barriers that both CTAs signal

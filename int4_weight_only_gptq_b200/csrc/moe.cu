@@ -392,7 +392,7 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
   }
   // no CTA leaves while another may still read its totals: this one has read
   // them, and waits for the others at its end
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  cluster_arrive();
   __syncthreads();  // first[] is complete
   for (int e = lane; e < E; e += 32) mine[e] += first[e];
   __syncwarp();
@@ -413,8 +413,7 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
       if (p < end) dest[p] = key[i] < E ? at + lower : -1;
     }
   }
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_wait();
 }
 
 // Rows: a warp takes 1024 values (four 16-byte chunks per lane) of one token,
