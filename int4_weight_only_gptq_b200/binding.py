@@ -385,6 +385,10 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
 # about as long as a call takes on the host, so their checks are kept short:
 # one expression per tensor, device indices instead of device objects, the
 # stream's handle without the stream object.
+#
+# stream=: a torch stream, or a raw handle, to run on instead of the current
+# stream.  The outputs that a call allocates are that stream's memory; the
+# caller orders the two streams' work itself.
 
 def _bad(t, name: str, dtype, index: int, shape=None):
     """Raises for a tensor that _fits refused, in _require's words."""
@@ -406,12 +410,10 @@ def _device_index(t, name: str) -> int:
     return t.get_device()
 
 
-def _call(fn, index: int, stream, *args):
-    """fn(*args, stream) with the tensors' device current; stream: a handle, or
-    None for the current stream."""
-    if stream is None:
-        # the handle of torch.cuda.current_stream(index), without the object
-        stream = torch._C._cuda_getCurrentRawStream(index)
+def _call(fn, index: int, *args):
+    """fn(*args, handle of the current stream) with the tensors' device current."""
+    # the handle of torch.cuda.current_stream(index), without the object
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, stream)
     else:
@@ -421,21 +423,38 @@ def _call(fn, index: int, stream, *args):
         _check(status)
 
 
-def _on_stream(fn, stream, out, *args):
+def _torch_stream(stream, device):
+    """A stream= argument as a torch stream: one already, or a raw handle."""
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
+        return stream
+    handle = stream.value or 0 if isinstance(stream, ctypes.c_void_p) else int(stream)
+    # 0 and 1 (cudaStreamLegacy) both name the legacy default stream, which
+    # torch would take for no handle at all
+    if handle in (0, 1):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _on_stream(fn, stream, *args):
     """fn(*args) with `stream` current, so that what it allocates is memory of
-    that stream (a block of the caller's stream may still be in use there),
-    kept from reuse until the caller's stream is done with it too.  `out` is
-    the caller's own buffer, if any."""
+    that stream (a block of the caller's stream may still be in use there).
+    Its results are kept from reuse until the caller's stream is done with them
+    too."""
     t = args[0]
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
-        raise ValueError(f"stream is on {stream.device}, expected {t.device}")
-    caller = torch.cuda.current_stream(stream.device)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return fn(*args)  # refuses it
+    stream = _torch_stream(stream, t.device)
+    caller = torch.cuda.current_stream(t.device)
+    if caller.cuda_stream == stream.cuda_stream:
+        return fn(*args)
     with torch.cuda.stream(stream):
         result = fn(*args)
-    if caller != stream:
-        for t in result if isinstance(result, tuple) else (result,):
-            if t is not out:
-                t.record_stream(caller)
+    given = [a for a in args if isinstance(a, torch.Tensor)]
+    for r in result if isinstance(result, tuple) else (result,):
+        if not any(r is a for a in given):
+            r.record_stream(caller)
     return result
 
 
@@ -449,8 +468,8 @@ def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
     int32): expert e's rows are offsets[e] .. offsets[e + 1] - 1, choice j of
     token m is row dest[m, j] (-1 if dropped), in the order of (m, j) within an
     expert.  The rows from offsets[n_experts] on keep what `out` holds."""
-    if isinstance(stream, torch.cuda.Stream):
-        return _on_stream(moe_sort, stream, out, x, expert_ids, n_experts, out)
+    if stream is not None:
+        return _on_stream(moe_sort, stream, x, expert_ids, n_experts, out)
     lib = _lib or load()
     dev = _device_index(x, "x")
     if not _fits(x, torch.float16, dev):
@@ -474,7 +493,7 @@ def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
                           dtype=torch.int32)
     dest = (torch.empty_like(expert_ids, dtype=torch.int32) if wide
             else torch.empty_like(expert_ids))
-    _call(lib.gptq_moe_sort, dev, stream, x.data_ptr(), expert_ids.data_ptr(), 8 if wide else 4,
+    _call(lib.gptq_moe_sort, dev, x.data_ptr(), expert_ids.data_ptr(), 8 if wide else 4,
           M, H, topk, n_experts, out.data_ptr(), offsets.data_ptr(), dest.data_ptr())
     return out, offsets, dest
 
@@ -485,8 +504,8 @@ def moe_combine(y_sorted: torch.Tensor, dest: torch.Tensor, weights: torch.Tenso
     the order of j, dropped choices (dest -1) left out.  y_sorted [R, H] FP16,
     dest [M, topk] int32 from moe_sort, weights [M, topk] FP32 or None for
     ones (then it is moe_sort's gradient, applied to that of x_sorted)."""
-    if isinstance(stream, torch.cuda.Stream):
-        return _on_stream(moe_combine, stream, out, y_sorted, dest, weights, out)
+    if stream is not None:
+        return _on_stream(moe_combine, stream, y_sorted, dest, weights, out)
     lib = _lib or load()
     dev = _device_index(y_sorted, "y_sorted")
     if not _fits(y_sorted, torch.float16, dev):
@@ -504,7 +523,7 @@ def moe_combine(y_sorted: torch.Tensor, dest: torch.Tensor, weights: torch.Tenso
         out = torch.empty((M, H), dtype=torch.float16, device=y_sorted.device)
     elif not _fits(out, torch.float16, dev) or out.shape != (M, H):
         _bad(out, "out", torch.float16, dev, (M, H))
-    _call(lib.gptq_moe_combine, dev, stream, y_sorted.data_ptr(), dest.data_ptr(),
+    _call(lib.gptq_moe_combine, dev, y_sorted.data_ptr(), dest.data_ptr(),
           None if weights is None else weights.data_ptr(), M, H, topk, R, out.data_ptr())
     return out
 
@@ -515,8 +534,8 @@ def moe_combine_backward(dout: torch.Tensor, y_sorted: torch.Tensor, dest: torch
     dweights [M, topk] FP32) from dout [M, H] FP16.  Rows that no entry of dest
     names keep what `out` (the buffer of dy_sorted) holds; dweights is 0 for
     dropped choices."""
-    if isinstance(stream, torch.cuda.Stream):
-        return _on_stream(moe_combine_backward, stream, out, dout, y_sorted, dest, weights, out)
+    if stream is not None:
+        return _on_stream(moe_combine_backward, stream, dout, y_sorted, dest, weights, out)
     lib = _lib or load()
     dev = _device_index(dout, "dout")
     if not _fits(dout, torch.float16, dev):
@@ -538,7 +557,7 @@ def moe_combine_backward(dout: torch.Tensor, y_sorted: torch.Tensor, dest: torch
     elif not _fits(out, torch.float16, dev) or out.shape != y_sorted.shape:
         _bad(out, "out", torch.float16, dev, (R, H))
     dweights = torch.empty_like(weights)
-    _call(lib.gptq_moe_combine_backward, dev, stream, dout.data_ptr(), y_sorted.data_ptr(),
+    _call(lib.gptq_moe_combine_backward, dev, dout.data_ptr(), y_sorted.data_ptr(),
           dest.data_ptr(), weights.data_ptr(), M, H, topk, R, out.data_ptr(),
           dweights.data_ptr())
     return out, dweights
@@ -565,7 +584,7 @@ def experts_shapes(rows, qweight, scales, offsets, group: int,
     return R, K, N, E
 
 
-def _experts(fn, rows, qweight, scales, offsets, group, out, stream, gradient, name):
+def _experts(fn, rows, qweight, scales, offsets, group, out, gradient, name):
     """Checks and output of an experts' product, and its library call; `fn`
     takes the entry's arguments without the kernel choice."""
     dev = _device_index(qweight, "qweight")
@@ -583,7 +602,7 @@ def _experts(fn, rows, qweight, scales, offsets, group, out, stream, gradient, n
         out = torch.empty(shape, dtype=torch.float16, device=rows.device)
     elif not _fits(out, torch.float16, dev) or out.shape != shape:
         _bad(out, "out", torch.float16, dev, shape)
-    _call(fn, dev, stream, rows.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
+    _call(fn, dev, rows.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
           offsets.data_ptr(), R, K, N, E, group, out.data_ptr())
     return out
 
@@ -597,14 +616,14 @@ def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     qweight [E, K/8, N] int32, scales [E, n_groups, N] FP16.  Rows that belong
     to no expert keep what `out` holds.  kernel and tile force the kernel: tests
     and benchmarks (KERNEL_DECODE takes a tile of 16 or 32 rows)."""
-    if isinstance(stream, torch.cuda.Stream):
-        return _on_stream(gemm_experts, stream, out, x_sorted, qweight, scales, offsets, group,
-                          out, None, kernel, tile)
+    if stream is not None:
+        return _on_stream(gemm_experts, stream, x_sorted, qweight, scales, offsets, group, out,
+                          None, kernel, tile)
     lib = _lib or load()
     fn = lib.gptq_w4a16_gemm_experts
     if kernel != KERNEL_AUTO or tile != 0:
         fn = lambda *args: lib.gptq_w4a16_gemm_experts_kernel(*args, kernel, tile)
-    return _experts(fn, x_sorted, qweight, scales, offsets, group, out, stream, False, "x_sorted")
+    return _experts(fn, x_sorted, qweight, scales, offsets, group, out, False, "x_sorted")
 
 
 def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
@@ -614,11 +633,11 @@ def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torc
     dy_sorted[r] . dequant(qweight[e], scales[e])^T, [R, K] FP16 from dy_sorted
     [R, N] FP16 (the packed weights are frozen and have no gradient); N up to
     65536, the length of the sums."""
-    if isinstance(stream, torch.cuda.Stream):
-        return _on_stream(gemm_experts_dx, stream, out, dy_sorted, qweight, scales, offsets,
-                          group, out)
+    if stream is not None:
+        return _on_stream(gemm_experts_dx, stream, dy_sorted, qweight, scales, offsets, group,
+                          out)
     return _experts((_lib or load()).gptq_w4a16_gemm_experts_dx, dy_sorted, qweight, scales,
-                    offsets, group, out, stream, True, "dy_sorted")
+                    offsets, group, out, True, "dy_sorted")
 
 
 def dequant(qweight: torch.Tensor, scales: torch.Tensor, group: int,
