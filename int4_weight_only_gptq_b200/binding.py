@@ -387,7 +387,8 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
 # stream's handle without the stream object.
 #
 # stream=: a torch stream, or a raw handle, to run on instead of the current
-# stream.  The outputs that a call allocates are that stream's memory; the
+# stream.  The outputs that a call allocates are that stream's memory, and no
+# tensor of the call is reused before both streams are done with it; the
 # caller orders the two streams' work itself.
 
 def _bad(t, name: str, dtype, index: int, shape=None):
@@ -441,7 +442,7 @@ def _on_stream(fn, stream, *args):
     """fn(*args) with `stream` current, so that what it allocates is memory of
     that stream (a block of the caller's stream may still be in use there).
     Its results are kept from reuse until the caller's stream is done with them
-    too."""
+    too, and the caller's tensors until `stream` is."""
     t = args[0]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return fn(*args)  # refuses it
@@ -452,6 +453,8 @@ def _on_stream(fn, stream, *args):
     with torch.cuda.stream(stream):
         result = fn(*args)
     given = [a for a in args if isinstance(a, torch.Tensor)]
+    for a in given:
+        a.record_stream(stream)
     for r in result if isinstance(result, tuple) else (result,):
         if not any(r is a for a in given):
             r.record_stream(caller)

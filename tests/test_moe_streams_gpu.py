@@ -74,6 +74,34 @@ def test_the_legacy_default_stream_by_its_handles(handle):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_inputs_are_kept_until_the_other_stream_is_done(raw):
+    """A caller may drop an input right after a call on another stream."""
+    rng = np.random.default_rng(23)
+    M, H, topk, E = 2048, 4096, 2, 4
+    ids = P.make_ids(rng, M, E, topk)
+    dest = cu(P.sort(ids, E)[1])
+    rows = cu(P.make_rows(rng, M * topk, H))
+    want = B.moe_combine(rows, dest)
+    side, out = torch.cuda.Stream(), torch.empty_like(want)
+    y, spare = rows.clone(), torch.empty_like(rows)
+    torch.cuda.synchronize()
+    del spare  # the only free block of y's size, so that the first of two takes it
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # about 50 ms
+    got = B.moe_combine(y, dest, out=out, stream=side.cuda_stream if raw else side)
+    lo = y.data_ptr()
+    del y
+    busy = not side.query()
+    others = [torch.empty_like(rows) for _ in range(2)]
+    assert busy, "the side stream had finished too early to show anything"
+    assert all(t.data_ptr() != lo for t in others)
+    for t in others:
+        t.fill_(float("nan"))
+    torch.cuda.synchronize()
+    assert got is out and torch.equal(got, want)
+
+
 def test_the_current_stream_by_name_or_handle_is_no_other_stream():
     args = layer_inputs(24)
     want = layer_on(None, *args)
