@@ -120,12 +120,66 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream_handle(stream, device):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
+def _current(device):
+    """The handle of torch.cuda.current_stream(device), without the object."""
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+
+
+# stream=: a torch stream, or a raw handle, to run on instead of the current
+# stream.  What a call allocates is that stream's memory, and no tensor of the
+# call is reused before both streams are done with it; the caller orders the
+# two streams' work itself.
+
+def _torch_stream(stream, device):
+    """A stream= argument as a torch stream: one already, or a raw handle."""
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
+        return stream
+    handle = stream.value or 0 if isinstance(stream, ctypes.c_void_p) else int(stream)
+    # 0 and 1 (cudaStreamLegacy) both name the legacy default stream, which
+    # torch would take for no handle at all
+    if handle in (0, 1):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _tensors(args) -> list:
+    """The tensors among args, those of its lists and tuples too."""
+    found = []
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            found.append(a)
+        elif isinstance(a, (list, tuple)):
+            found += _tensors(a)
+    return found
+
+
+def _on_stream(fn, stream, *args):
+    """fn(*args) with `stream` current, so that what it allocates is memory of
+    that stream (a block of the caller's stream may still be in use there).
+    Its results are kept from reuse until the caller's stream is done with them
+    too, and the caller's tensors until `stream` is."""
+    t = args[0]
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return fn(*args)  # refuses it
+    stream, index = _torch_stream(stream, t.device), t.get_device()
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index):
+        return fn(*args)
+    caller = torch.cuda.current_stream(index)
+    with torch.cuda.device(index):  # set_stream makes the stream's device current
+        torch.cuda.set_stream(stream)
+        try:
+            result = fn(*args)
+        finally:
+            torch.cuda.set_stream(caller)
+    given = _tensors(args)
+    for a in given:
+        a.record_stream(stream)
+    for r in _tensors((result,)):
+        if not any(r is a for a in given):
+            r.record_stream(caller)
+    return result
 
 
 def _as_bits16(t: torch.Tensor) -> torch.Tensor:
@@ -197,6 +251,9 @@ def gemm(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, group: in
          out: torch.Tensor | None = None, stream=None, kernel: int = KERNEL_AUTO,
          decode_splits: int = 0) -> torch.Tensor:
     """Y[M, N] = x[M, K] . dequant(qweight[K/8, N], scales[n_groups, N]) (FP16)."""
+    if stream is not None:
+        return _on_stream(gemm, stream, x, qweight, scales, group, out, None, kernel,
+                          decode_splits)
     lib = load()
     dev = qweight.device
     _require(qweight, "qweight", lambda d: d == torch.int32, None)
@@ -208,8 +265,7 @@ def gemm(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, group: in
     else:
         _require(out, "out", lambda d: d == torch.float16, dev)
         _check_shape(out, "out", (M, N))
-    s = _stream_handle(stream, dev)
-    args = (_ptr(x), _ptr(qweight), _ptr(scales), M, K, N, group, _ptr(out), s)
+    args = (_ptr(x), _ptr(qweight), _ptr(scales), M, K, N, group, _ptr(out), _current(dev))
     with torch.cuda.device(dev):  # the library works on the current device
         if decode_splits:
             _check(lib.gptq_w4a16_gemm_decode_splits(*args, decode_splits))
@@ -224,6 +280,8 @@ def gemm_grouped(x: torch.Tensor, qweights, scales, group: int, outs=None,
                  stream=None) -> list:
     """Y_i = x . dequant(qweights[i], scales[i]) for linears sharing x (one
     decode launch for M <= DECODE_MAX_M)."""
+    if stream is not None:
+        return _on_stream(gemm_grouped, stream, x, qweights, scales, group, outs)
     lib = load()
     if not 1 <= len(qweights) <= MAX_GROUPED or len(scales) != len(qweights):
         raise ValueError(f"need 1..{MAX_GROUPED} linears with one scales tensor each")
@@ -256,7 +314,7 @@ def gemm_grouped(x: torch.Tensor, qweights, scales, group: int, outs=None,
     ya = (ctypes.c_void_p * count)(*[_ptr(o) for o in outs])
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_grouped(_ptr(x), qa, sa, na, count, M, K, group, ya,
-                                           _stream_handle(stream, dev)))
+                                           _current(dev)))
     return outs
 
 
@@ -265,6 +323,8 @@ def gemm_asym(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
               stream=None) -> torch.Tensor:
     """Y = x . W, W = fp16((q - z) * s) with zeros packed in qzeros
     [n_groups, N/8] int32 (eight per word along N); N % 32 == 0."""
+    if stream is not None:
+        return _on_stream(gemm_asym, stream, x, qweight, scales, qzeros, group, out)
     lib = load()
     dev = qweight.device
     _require(qweight, "qweight", lambda d: d == torch.int32, None)
@@ -282,7 +342,7 @@ def gemm_asym(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
         _check_shape(out, "out", (M, N))
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_asym(_ptr(x), _ptr(qweight), _ptr(scales), _ptr(qzeros), M,
-                                        K, N, group, _ptr(out), _stream_handle(stream, dev)))
+                                        K, N, group, _ptr(out), _current(dev)))
     return out
 
 
@@ -304,6 +364,8 @@ def gemm_gidx(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
     order): g_idx [K] int32 with entries in 0 .. n_groups - 1, scales
     [n_groups, N], n_groups <= GIDX_MAX_GROUPS.  An out-of-range index is
     reported by device_error() as GPTQ_ERR_INDEX."""
+    if stream is not None:
+        return _on_stream(gemm_gidx, stream, x, qweight, scales, g_idx, out)
     lib = load()
     dev = qweight.device
     _require(qweight, "qweight", lambda d: d == torch.int32, None)
@@ -318,7 +380,7 @@ def gemm_gidx(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
         _check_shape(out, "out", (M, N))
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_gidx(_ptr(x), _ptr(qweight), _ptr(scales), _ptr(g_idx), M, K,
-                                        N, ng, _ptr(out), _stream_handle(stream, dev)))
+                                        N, ng, _ptr(out), _current(dev)))
     return out
 
 
@@ -328,6 +390,9 @@ def gemm_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, grou
     """Y = x . dequant(qweight, scales) + fp16(x . lora_a^T) . lora_b^T (FP16),
     lora_a [rank, K], lora_b [N, rank] with the adapter's scaling applied;
     t_work [M, rank] receives fp16(x . lora_a^T)."""
+    if stream is not None:
+        return _on_stream(gemm_lora, stream, x, qweight, scales, group, lora_a, lora_b, t_work,
+                          out)
     lib = load()
     dev = qweight.device
     _require(qweight, "qweight", lambda d: d == torch.int32, None)
@@ -350,7 +415,7 @@ def gemm_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, grou
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_lora(_ptr(x), _ptr(qweight), _ptr(scales), M, K, N, group,
                                         _ptr(lora_a), _ptr(lora_b), rank, _ptr(t_work),
-                                        _ptr(out), _stream_handle(stream, dev)))
+                                        _ptr(out), _current(dev)))
     return out
 
 
@@ -360,6 +425,9 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     """gemm_lora with T kept in the library's static device buffer (no work
     tensor; M * rank * 2 <= LORA_SCRATCH_BYTES; calls that may overlap in time
     share the buffer and race)."""
+    if stream is not None:
+        return _on_stream(gemm_lora_noalloc, stream, x, qweight, scales, group, lora_a, lora_b,
+                          out)
     lib = load()
     dev = qweight.device
     _require(qweight, "qweight", lambda d: d == torch.int32, None)
@@ -377,7 +445,7 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_lora_noalloc(_ptr(x), _ptr(qweight), _ptr(scales), M, K, N,
                                                 group, _ptr(lora_a), _ptr(lora_b), rank,
-                                                _ptr(out), _stream_handle(stream, dev)))
+                                                _ptr(out), _current(dev)))
     return out
 
 
@@ -385,11 +453,6 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
 # about as long as a call takes on the host, so their checks are kept short:
 # one expression per tensor, device indices instead of device objects, the
 # stream's handle without the stream object.
-#
-# stream=: a torch stream, or a raw handle, to run on instead of the current
-# stream.  The outputs that a call allocates are that stream's memory, and no
-# tensor of the call is reused before both streams are done with it; the
-# caller orders the two streams' work itself.
 
 def _bad(t, name: str, dtype, index: int, shape=None):
     """Raises for a tensor that _fits refused, in _require's words."""
@@ -422,43 +485,6 @@ def _call(fn, index: int, *args):
             status = fn(*args, stream)
     if status != 0:
         _check(status)
-
-
-def _torch_stream(stream, device):
-    """A stream= argument as a torch stream: one already, or a raw handle."""
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, expected {device}")
-        return stream
-    handle = stream.value or 0 if isinstance(stream, ctypes.c_void_p) else int(stream)
-    # 0 and 1 (cudaStreamLegacy) both name the legacy default stream, which
-    # torch would take for no handle at all
-    if handle in (0, 1):
-        return torch.cuda.default_stream(device)
-    return torch.cuda.ExternalStream(handle, device=device)
-
-
-def _on_stream(fn, stream, *args):
-    """fn(*args) with `stream` current, so that what it allocates is memory of
-    that stream (a block of the caller's stream may still be in use there).
-    Its results are kept from reuse until the caller's stream is done with them
-    too, and the caller's tensors until `stream` is."""
-    t = args[0]
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        return fn(*args)  # refuses it
-    stream = _torch_stream(stream, t.device)
-    caller = torch.cuda.current_stream(t.device)
-    if caller.cuda_stream == stream.cuda_stream:
-        return fn(*args)
-    with torch.cuda.stream(stream):
-        result = fn(*args)
-    given = [a for a in args if isinstance(a, torch.Tensor)]
-    for a in given:
-        a.record_stream(stream)
-    for r in result if isinstance(result, tuple) else (result,):
-        if not any(r is a for a in given):
-            r.record_stream(caller)
-    return result
 
 
 def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
@@ -646,6 +672,8 @@ def gemm_experts_dx(dy_sorted: torch.Tensor, qweight: torch.Tensor, scales: torc
 def dequant(qweight: torch.Tensor, scales: torch.Tensor, group: int,
             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """W[K, N] = fp16((q - 8) * s): the debugging entry."""
+    if stream is not None:
+        return _on_stream(dequant, stream, qweight, scales, group, out)
     lib = load()
     dev = qweight.device
     _require(qweight, "qweight", lambda d: d == torch.int32, None)
@@ -663,7 +691,7 @@ def dequant(qweight: torch.Tensor, scales: torch.Tensor, group: int,
         _check_shape(out, "out", (K, N))
     with torch.cuda.device(dev):
         _check(lib.gptq_dequant(_ptr(qweight), _ptr(scales), K, N, group, _ptr(out),
-                                _stream_handle(stream, dev)))
+                                _current(dev)))
     return out
 
 

@@ -12,6 +12,13 @@ CALLS = {
     "moe_combine_backward": ("dout", "y_sorted", "dest", "weights"),
     "gemm_experts": ("x_sorted", "qweight", "scales", "offsets", 32),
     "gemm_experts_dx": ("dy_sorted", "qweight", "scales", "offsets", 32),
+    "gemm": ("x", "qweight", "scales", 32),
+    "gemm_grouped": ("x", ["qweight"], ["scales"], 32),
+    "gemm_asym": ("x", "qweight", "scales", "qzeros", 32),
+    "gemm_gidx": ("x", "qweight", "scales", "g_idx"),
+    "gemm_lora": ("x", "qweight", "scales", 32, "lora_a", "lora_b"),
+    "gemm_lora_noalloc": ("x", "qweight", "scales", 32, "lora_a", "lora_b"),
+    "dequant": ("qweight", "scales", 32),
 }
 
 
@@ -21,7 +28,7 @@ def test_raw_handles_take_the_path_of_streams(name, stream, monkeypatch):
     """A handle, too, moves what a call allocates to its stream."""
     fn, seen = getattr(B, name), []
     monkeypatch.setattr(B, "_on_stream", lambda f, s, *args: seen.append((f, s, args)))
-    fn(*CALLS[name], out="out", stream=stream)
+    fn(*CALLS[name], **{"outs" if name == "gemm_grouped" else "out": "out"}, stream=stream)
     (f, s, args), = seen
     assert f is fn and s is stream
     assert args[:len(CALLS[name])] == CALLS[name] and "out" in args
