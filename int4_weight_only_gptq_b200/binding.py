@@ -120,6 +120,13 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _int32(value):
+    """`value` as the library shall see it: ctypes keeps the low bits of a
+    number that does not fit, which may be a valid one that was not checked
+    here; the least number instead is none of its choices."""
+    return value if -2 ** 31 <= value < 2 ** 31 else -2 ** 31
+
+
 def _current(device):
     """The handle of torch.cuda.current_stream(device), without the object."""
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
@@ -265,14 +272,15 @@ def gemm(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, group: in
     else:
         _require(out, "out", lambda d: d == torch.float16, dev)
         _check_shape(out, "out", (M, N))
-    args = (_ptr(x), _ptr(qweight), _ptr(scales), M, K, N, group, _ptr(out), _current(dev))
+    args = (_ptr(x), _ptr(qweight), _ptr(scales), M, K, N, _int32(group), _ptr(out),
+            _current(dev))
     with torch.cuda.device(dev):  # the library works on the current device
         if decode_splits:
-            _check(lib.gptq_w4a16_gemm_decode_splits(*args, decode_splits))
+            _check(lib.gptq_w4a16_gemm_decode_splits(*args, _int32(decode_splits)))
         elif kernel == KERNEL_AUTO:
             _check(lib.gptq_w4a16_gemm(*args))
         else:
-            _check(lib.gptq_w4a16_gemm_kernel(*args, kernel))
+            _check(lib.gptq_w4a16_gemm_kernel(*args, _int32(kernel)))
     return out
 
 
@@ -313,7 +321,7 @@ def gemm_grouped(x: torch.Tensor, qweights, scales, group: int, outs=None,
     na = (ctypes.c_int64 * count)(*Ns)
     ya = (ctypes.c_void_p * count)(*[_ptr(o) for o in outs])
     with torch.cuda.device(dev):
-        _check(lib.gptq_w4a16_gemm_grouped(_ptr(x), qa, sa, na, count, M, K, group, ya,
+        _check(lib.gptq_w4a16_gemm_grouped(_ptr(x), qa, sa, na, count, M, K, _int32(group), ya,
                                            _current(dev)))
     return outs
 
@@ -342,7 +350,7 @@ def gemm_asym(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
         _check_shape(out, "out", (M, N))
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_asym(_ptr(x), _ptr(qweight), _ptr(scales), _ptr(qzeros), M,
-                                        K, N, group, _ptr(out), _current(dev)))
+                                        K, N, _int32(group), _ptr(out), _current(dev)))
     return out
 
 
@@ -413,9 +421,9 @@ def gemm_lora(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor, grou
         _require(out, "out", lambda d: d == torch.float16, dev)
         _check_shape(out, "out", (M, N))
     with torch.cuda.device(dev):
-        _check(lib.gptq_w4a16_gemm_lora(_ptr(x), _ptr(qweight), _ptr(scales), M, K, N, group,
-                                        _ptr(lora_a), _ptr(lora_b), rank, _ptr(t_work),
-                                        _ptr(out), _current(dev)))
+        _check(lib.gptq_w4a16_gemm_lora(_ptr(x), _ptr(qweight), _ptr(scales), M, K, N,
+                                        _int32(group), _ptr(lora_a), _ptr(lora_b), rank,
+                                        _ptr(t_work), _ptr(out), _current(dev)))
     return out
 
 
@@ -444,7 +452,7 @@ def gemm_lora_noalloc(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tens
         _check_shape(out, "out", (M, N))
     with torch.cuda.device(dev):
         _check(lib.gptq_w4a16_gemm_lora_noalloc(_ptr(x), _ptr(qweight), _ptr(scales), M, K, N,
-                                                group, _ptr(lora_a), _ptr(lora_b), rank,
+                                                _int32(group), _ptr(lora_a), _ptr(lora_b), rank,
                                                 _ptr(out), _current(dev)))
     return out
 
@@ -517,13 +525,13 @@ def moe_sort(x: torch.Tensor, expert_ids: torch.Tensor, n_experts: int,
         out = torch.empty((M * topk, H), dtype=torch.float16, device=x.device)
     elif not _fits(out, torch.float16, dev) or out.shape != (M * topk, H):
         _bad(out, "out", torch.float16, dev, (M * topk, H))
-    # (the library refuses any other number of experts)
-    offsets = x.new_empty(n_experts + 1 if 0 < n_experts <= MOE_MAX_EXPERTS else 1,
-                          dtype=torch.int32)
+    # (the library refuses 0, and shall not see the low bits of a larger number)
+    E = n_experts if 0 < n_experts <= MOE_MAX_EXPERTS else 0
+    offsets = x.new_empty(E + 1, dtype=torch.int32)
     dest = (torch.empty_like(expert_ids, dtype=torch.int32) if wide
             else torch.empty_like(expert_ids))
     _call(lib.gptq_moe_sort, dev, x.data_ptr(), expert_ids.data_ptr(), 8 if wide else 4,
-          M, H, topk, n_experts, out.data_ptr(), offsets.data_ptr(), dest.data_ptr())
+          M, H, topk, E, out.data_ptr(), offsets.data_ptr(), dest.data_ptr())
     return out, offsets, dest
 
 
@@ -632,7 +640,7 @@ def _experts(fn, rows, qweight, scales, offsets, group, out, gradient, name):
     elif not _fits(out, torch.float16, dev) or out.shape != shape:
         _bad(out, "out", torch.float16, dev, shape)
     _call(fn, dev, rows.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
-          offsets.data_ptr(), R, K, N, E, group, out.data_ptr())
+          offsets.data_ptr(), R, K, N, E, _int32(group), out.data_ptr())
     return out
 
 
@@ -651,7 +659,8 @@ def gemm_experts(x_sorted: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
     lib = _lib or load()
     fn = lib.gptq_w4a16_gemm_experts
     if kernel != KERNEL_AUTO or tile != 0:
-        fn = lambda *args: lib.gptq_w4a16_gemm_experts_kernel(*args, kernel, tile)
+        fn = lambda *args: lib.gptq_w4a16_gemm_experts_kernel(*args, _int32(kernel),
+                                                              _int32(tile))
     return _experts(fn, x_sorted, qweight, scales, offsets, group, out, False, "x_sorted")
 
 
@@ -690,7 +699,7 @@ def dequant(qweight: torch.Tensor, scales: torch.Tensor, group: int,
         _require(out, "out", lambda d: d == torch.float16, dev)
         _check_shape(out, "out", (K, N))
     with torch.cuda.device(dev):
-        _check(lib.gptq_dequant(_ptr(qweight), _ptr(scales), K, N, group, _ptr(out),
+        _check(lib.gptq_dequant(_ptr(qweight), _ptr(scales), K, N, _int32(group), _ptr(out),
                                 _current(dev)))
     return out
 
@@ -699,7 +708,7 @@ def select(M: int, K: int, N: int, group: int) -> tuple[int, int]:
     """(kernel_id, split_k) the dispatcher picks for this shape."""
     lib = load()
     k, s = _i32(-1), _i32(-1)
-    _check(lib.gptq_w4a16_select(M, K, N, group, ctypes.byref(k), ctypes.byref(s)))
+    _check(lib.gptq_w4a16_select(M, K, N, _int32(group), ctypes.byref(k), ctypes.byref(s)))
     return k.value, s.value
 
 
