@@ -331,6 +331,8 @@ __global__ void __cluster_dims__(kPlaceCtas, 1, 1) __launch_bounds__(kPlaceThrea
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = (int)cluster_ctarank();
   wait_previous_grid();
+  // After the wait, never before: sort_rows_kernel reads x as soon as every CTA
+  // has said this, so it must mean that the work before this launch is done.
   let_next_grid_start();
   const int64_t w = (int64_t)cta * kPlaceWarps + warp;
   constexpr int64_t W = kPlaceCtas * kPlaceWarps;
@@ -613,8 +615,10 @@ __global__ void __launch_bounds__(kBackThreads)
   }
 }
 
-// A launch that may begin while the previous kernel of the stream ends: every
-// kernel above waits for it before it reads or writes anything.
+// A launch that may begin while the previous kernel of the stream ends.  Every
+// kernel above waits for that one before it reads or writes anything, but for
+// sort_rows_kernel, which reads x before it waits for the places' launch (see
+// there for why x is complete).
 struct Launch {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
