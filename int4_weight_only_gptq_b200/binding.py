@@ -1,10 +1,14 @@
 """Python binding of libgptq_w4a16.so (ctypes; argument marshalling only).
 
 Every step of the layer runs in the library's CUDA kernels.  PyTorch supplies
-device memory and the current stream; this module checks tensor dtypes and
-devices, passes raw pointers, and turns status codes into exceptions.  There is
-no CPU path: if the library is missing or the device is not sm_100, calls
-raise.
+device memory and the current stream; this module checks tensor dtypes,
+devices and shapes, passes raw pointers, and turns status codes into
+exceptions.  There is no CPU path: if the library is missing or the device is
+not sm_100, calls raise.
+
+No call takes part in autograd: outputs carry no history, whatever the inputs
+require.  A training step calls the gradients (gemm_experts_dx, moe_combine and
+moe_combine_backward) itself, from an autograd.Function of its own for instance.
 """
 from __future__ import annotations
 
@@ -570,7 +574,8 @@ def moe_combine_backward(dout: torch.Tensor, y_sorted: torch.Tensor, dest: torch
     """The gradients of moe_combine with weights: (dy_sorted [R, H] FP16,
     dweights [M, topk] FP32) from dout [M, H] FP16.  Rows that no entry of dest
     names keep what `out` (the buffer of dy_sorted) holds; dweights is 0 for
-    dropped choices."""
+    dropped choices.  Entries of dest that are not dropped must differ from
+    each other, as moe_sort's do: two that name one row both write it."""
     if stream is not None:
         return _on_stream(moe_combine_backward, stream, dout, y_sorted, dest, weights, out)
     lib = _lib or load()

@@ -24,7 +24,7 @@
 // * One elected lane issues the MMAs into one of two accumulators; four warps
 //   of their own read a finished item out and store it while the next one is
 //   multiplied.  An MMA of 16 tokens takes 15 cycles, into one accumulator or
-//   into four in turn; a stage's sixteen with their commits 310 alone, 470
+//   into four in turn; a stage's sixteen with their commits 320 alone, 460
 //   beside warps that keep the issue slots busy.
 // * Few items (splits > 1): the CTAs of a cluster share one item, each taking
 //   a range of K, and add their partial sums in rank order through
